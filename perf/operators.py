@@ -296,6 +296,12 @@ def _store(x, slots, P, codes, scale):
     codes.view(torch.uint8).index_put_((page[:, None], heads, off[:, None]), q.view(torch.uint8))
 
 
+def _bf16(x):
+    """64-bit values to bf16 in one rounding (a cast by way of 32 bits may round twice)."""
+    m, e = torch.frexp(x)
+    return torch.ldexp(torch.round(m * 256.0), e - 8).to(torch.bfloat16)
+
+
 def _rotate(x, pos):
     """RMS(RoPE(x)) of rows x (B, heads, D) at positions pos (B,), in 64 bits, rounded to bf16."""
     D = x.shape[-1]
@@ -303,7 +309,7 @@ def _rotate(x, pos):
     ang = (pos.double()[:, None] * theta)[:, None]
     a, b = x[..., :D // 2].double(), x[..., D // 2:].double()
     y = torch.cat([a * ang.cos() - b * ang.sin(), a * ang.sin() + b * ang.cos()], -1)
-    return (y / torch.sqrt(y.square().mean(-1, keepdim=True) + EPS)).to(torch.bfloat16)
+    return _bf16(y / torch.sqrt(y.square().mean(-1, keepdim=True) + EPS))
 
 
 def _decode(s):
@@ -319,7 +325,7 @@ def _decode(s):
         vp = s["v"]
         if s["ve"] is not None:
             g = 2.0 * torch.sigmoid((s["gate_x"].double()[:, :, None] * s["Wg"].double()[None]).sum(1))
-            vp = (vp.double() + g[..., None] * s["ve"].double()).to(torch.bfloat16)
+            vp = _bf16(vp.double() + g[..., None] * s["ve"].double())
         page = torch.where(n > 0, table.gather(1, (pos // P)[:, None])[:, 0], dummy)
         off = pos % P
         heads = torch.arange(Hkv, device="cuda")[None]
@@ -432,6 +438,12 @@ def _nearest(x):
     return (torch.round(x / step) * step).clamp(-CODE_MAX, CODE_MAX)
 
 
+def _eight(x):
+    """64-bit values with eight significant bits, ties to even."""
+    step = torch.exp2(torch.floor(torch.log2(x.abs().clamp_min(1e-30))) - 7.0)
+    return torch.round(x / step) * step
+
+
 def _fit(amax):
     """The exponent of the smallest power of two that brings amax within 448, one element at a time."""
     def one(a):
@@ -467,7 +479,7 @@ def _turned(x, pos):
     w = torch.tensor([pos * ROPE_BASE ** (-2.0 * i / D) for i in range(D // 2)], dtype=torch.float64, device="cuda")
     z = torch.complex(x[:, :D // 2].double(), x[:, D // 2:].double()) * torch.polar(torch.ones_like(w), w)
     y = torch.cat([z.real, z.imag], 1)
-    return (y * (y.square().mean(1, keepdim=True) + EPS) ** -0.5).to(torch.bfloat16).double()
+    return _eight(y * (y.square().mean(1, keepdim=True) + EPS) ** -0.5)
 
 
 def exact(case, seed):
@@ -523,7 +535,7 @@ def exact(case, seed):
             vp = s["v"][b].double()
             if s["ve"] is not None:
                 z = s["gate_x"][b].double() @ s["Wg"].double()
-                vp = (vp + (2.0 / (1.0 + torch.exp(-z)))[:, None] * s["ve"][b].double()).to(torch.bfloat16).double()
+                vp = _eight(vp + (2.0 / (1.0 + torch.exp(-z)))[:, None] * s["ve"][b].double())
             for i, (which, row) in enumerate((("k", _turned(s["k"][b], n - 1)), ("v", vp))):
                 now = _append(s, which, table[b][(n - 1) // P], (n - 1) % P, row[None])
                 whole[which][:, last:last + now.shape[1]] = now
