@@ -95,6 +95,16 @@ def _load() -> ctypes.CDLL:
     lib.swa_attn_qkv_prologue.restype = I
     lib.swa_attn_fwd_x.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, Z, P]
     lib.swa_attn_fwd_x.restype = I
+    lib.swa_attn_kv_pages.argtypes = [P] * 12 + [I] * 6 + [P]
+    lib.swa_attn_kv_pages.restype = I
+    lib.swa_attn_kv8_write.argtypes = [P] * 7 + [I] * 6 + [P]
+    lib.swa_attn_kv8_write.restype = I
+    lib.swa_attn_kv8_read.argtypes = [P] * 7 + [I] * 6 + [P]
+    lib.swa_attn_kv8_read.restype = I
+    lib.swa_attn_kv8_decode_workspace_bytes.argtypes = [I, I, I, I]
+    lib.swa_attn_kv8_decode_workspace_bytes.restype = Z
+    lib.swa_attn_kv8_decode.argtypes = [P] * 15 + [I] * 8 + [F, F, P, Z, P]
+    lib.swa_attn_kv8_decode.restype = I
     lib.swa_attn_selftest_wait.argtypes = [I, P]
     lib.swa_attn_selftest_wait.restype = I
     lib.swa_attn_set_wait_limit_ms.argtypes = [I]
@@ -254,6 +264,37 @@ def swa_attn_fwd_x(x, Wqkv, ve, Wg, out, lse, B, T, C, H, Hkv, D, window, rope_b
                    ws_bytes, stream) -> int:
     return _lib.swa_attn_fwd_x(x, Wqkv, ve, Wg, out, lse, B, T, C, H, Hkv, D, window, rope_base, eps,
                                workspace, ws_bytes, stream)
+
+
+def swa_attn_kv_pages(block_table, kv_len, first_page, pool, n_new, ring, block_table_out, kv_len_out, first_page_out,
+                      pool_out, slots, step_len, B, T, max_pages, n_pages, page_size, window, stream) -> int:
+    return _lib.swa_attn_kv_pages(block_table, kv_len, first_page, pool, n_new, ring, block_table_out, kv_len_out,
+                                  first_page_out, pool_out, slots, step_len, B, T, max_pages, n_pages, page_size,
+                                  window, stream)
+
+
+def swa_attn_kv8_write(kh, vp, slots, k_cache, v_cache, k_scale, v_scale, B, T, Hkv, D, n_pages, page_size,
+                       stream) -> int:
+    return _lib.swa_attn_kv8_write(kh, vp, slots, k_cache, v_cache, k_scale, v_scale, B, T, Hkv, D, n_pages,
+                                   page_size, stream)
+
+
+def swa_attn_kv8_read(slots, k_cache, v_cache, k_scale, v_scale, kh, vp, B, T, Hkv, D, n_pages, page_size,
+                      stream) -> int:
+    return _lib.swa_attn_kv8_read(slots, k_cache, v_cache, k_scale, v_scale, kh, vp, B, T, Hkv, D, n_pages,
+                                  page_size, stream)
+
+
+def swa_attn_kv8_decode_workspace_bytes(B, H, Hkv, D) -> int:
+    return int(_lib.swa_attn_kv8_decode_workspace_bytes(B, H, Hkv, D))
+
+
+def swa_attn_kv8_decode(q, k, v, ve, gate_x, Wg, k_cache, v_cache, k_scale, v_scale, block_table, seq_len, doc_start,
+                        out, lse, B, H, Hkv, D, n_pages, page_size, max_pages, window, rope_base, eps, workspace,
+                        ws_bytes, stream) -> int:
+    return _lib.swa_attn_kv8_decode(q, k, v, ve, gate_x, Wg, k_cache, v_cache, k_scale, v_scale, block_table, seq_len,
+                                    doc_start, out, lse, B, H, Hkv, D, n_pages, page_size, max_pages, window,
+                                    rope_base, eps, workspace, ws_bytes, stream)
 
 
 def swa_attn_selftest_wait(limit_ms: int, stream=None) -> int:
@@ -566,6 +607,189 @@ def forward_x(x, Wqkv, H: int, Hkv: int, D: int, window: int = 0, ve=None, Wg=No
     return out, lse
 
 
+def _on_stream(stream, dev):
+    """Context in which the current device is `dev` and the current stream the one the call runs on
+    (`stream`: a torch stream on that device, a raw handle, or None for the device's current stream), so
+    that what the call allocates belongs to that stream; and the stream's handle."""
+    import torch
+    if stream is None:
+        return torch.cuda.device(dev), torch.cuda.current_stream(dev).cuda_stream
+    handle = _stream_handle(stream, dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(handle, device=dev)
+    return torch.cuda.stream(stream), handle
+
+
+def _check_kv8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev):
+    """The paged cache of Hkv heads of D features; returns (n_pages, page_size)."""
+    import torch
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be (n_pages, Hkv, page_size, D)")
+    n_pages, page_size = k_cache.shape[0], k_cache.shape[2]
+    shape = (n_pages, Hkv, page_size, D)
+    _want("k_cache", k_cache, shape, torch.float8_e4m3fn, dev)
+    _want("v_cache", v_cache, shape, torch.float8_e4m3fn, dev)
+    _want("k_scale", k_scale, (n_pages, Hkv), torch.float32, dev)
+    _want("v_scale", v_scale, (n_pages, Hkv), torch.float32, dev)
+    return n_pages, page_size
+
+
+def kv_pages(block_table, kv_len, first_page, ring, pool, n_new, page_size: int, window: int = 0, T: int = 1, *,
+             out=None, slots=None, step_len=None, stream=None):
+    """One step of the page allocator of a paged cache (C call swa_attn_kv_pages), from int32 CUDA tensors:
+    block_table (B, max_pages), kv_len, first_page, n_new (B,), ring (n_pages,), pool (2,).  n_new holds the tokens
+    that join each request (at most T; 0: idle, negative: the request has ended).  A new cache starts with block_table
+    -1, kv_len and first_page 0, ring = arange(n_pages) and pool = [0, n_pages].
+    The state is updated in place, or written to ``out`` = (block_table, kv_len, first_page, pool) (the ring
+    is always updated in place).  Returns (slots (B, T), step_len (B,)): the slot of every new token (-1: none) and
+    the length of every request that was served, 0 for the others (the seq_len of ``decode_kv8``).
+    ``slots`` and ``step_len`` may be passed in (then T is that tensor's)."""
+    import torch
+    i32 = torch.int32
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be (B, max_pages)")
+    B, max_pages = block_table.shape
+    dev = block_table.device
+    if out is None:
+        out = (block_table, kv_len, first_page, pool)
+    if len(out) != 4:
+        raise ValueError("out is (block_table, kv_len, first_page, pool)")
+    if ring.dim() != 1:
+        raise ValueError("ring must be (n_pages,)")
+    for name, t, shape in (("block_table", block_table, (B, max_pages)), ("kv_len", kv_len, (B,)),
+                           ("first_page", first_page, (B,)), ("pool", pool, (2,)), ("n_new", n_new, (B,)),
+                           ("ring", ring, ring.shape), ("out[0]", out[0], (B, max_pages)), ("out[1]", out[1], (B,)),
+                           ("out[2]", out[2], (B,)), ("out[3]", out[3], (2,))):
+        _want(name, t, shape, i32, dev)
+    if slots is not None:
+        if slots.dim() != 2:
+            raise ValueError("slots must be (B, T)")
+        T = slots.shape[1]
+        _want("slots", slots, (B, T), i32, dev)
+    if step_len is not None:
+        _want("step_len", step_len, (B,), i32, dev)
+    ctx, st = _on_stream(stream, dev)
+    with ctx:
+        if slots is None:
+            slots = torch.empty((B, T), dtype=i32, device=dev)
+        if step_len is None:
+            step_len = torch.empty((B,), dtype=i32, device=dev)
+        rc = swa_attn_kv_pages(_ptr(block_table), _ptr(kv_len), _ptr(first_page), _ptr(pool), _ptr(n_new), _ptr(ring),
+                               _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), _ptr(slots), _ptr(step_len),
+                               B, T, max_pages, ring.shape[0], int(page_size), int(window), st)
+    if rc != SWA_OK:
+        raise SwaError(rc, "swa_attn_kv_pages")
+    return slots, step_len
+
+
+def kv8_write(kh, vp, slots, k_cache, v_cache, k_scale, v_scale, *, stream=None) -> None:
+    """khat, v' rows kh, vp bf16 (B, T, Hkv, D) into the slots int32 (B, T) of a paged 8-bit cache (C call
+    swa_attn_kv8_write): k_cache, v_cache float8_e4m3fn (n_pages, Hkv, page_size, D), k_scale, v_scale fp32
+    (n_pages, Hkv), updated in place.  Rows with a negative slot are skipped."""
+    import torch
+    if kh.dim() != 4:
+        raise ValueError("kh and vp must be (B, T, Hkv, D)")
+    B, T, Hkv, D = kh.shape
+    dev = kh.device
+    _want("kh", kh, (B, T, Hkv, D), torch.bfloat16)
+    _want("vp", vp, (B, T, Hkv, D), torch.bfloat16, dev)
+    _want("slots", slots, (B, T), torch.int32, dev)
+    n_pages, page_size = _check_kv8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev)
+    ctx, st = _on_stream(stream, dev)
+    with ctx:
+        rc = swa_attn_kv8_write(_ptr(kh), _ptr(vp), _ptr(slots), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                _ptr(v_scale), B, T, Hkv, D, n_pages, page_size, st)
+    if rc != SWA_OK:
+        raise SwaError(rc, "swa_attn_kv8_write")
+
+
+def kv8_read(slots, k_cache, v_cache, k_scale, v_scale, *, kh=None, vp=None, stream=None):
+    """The cached khat and v' of the slots int32 (B, T) as bf16 (B, T, Hkv, D), exact (C call
+    swa_attn_kv8_read); zero rows for negative slots.  Returns (kh, vp)."""
+    import torch
+    if slots.dim() != 2 or k_cache.dim() != 4:
+        raise ValueError("slots must be (B, T), the caches (n_pages, Hkv, page_size, D)")
+    B, T = slots.shape
+    Hkv, D = k_cache.shape[1], k_cache.shape[3]
+    dev = slots.device
+    _want("slots", slots, (B, T), torch.int32)
+    n_pages, page_size = _check_kv8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev)
+    for name, t in (("kh", kh), ("vp", vp)):
+        if t is not None:
+            _want(name, t, (B, T, Hkv, D), torch.bfloat16, dev)
+    ctx, st = _on_stream(stream, dev)
+    with ctx:
+        if kh is None:
+            kh = torch.empty((B, T, Hkv, D), dtype=torch.bfloat16, device=dev)
+        if vp is None:
+            vp = torch.empty((B, T, Hkv, D), dtype=torch.bfloat16, device=dev)
+        rc = swa_attn_kv8_read(_ptr(slots), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(kh),
+                               _ptr(vp), B, T, Hkv, D, n_pages, page_size, st)
+    if rc != SWA_OK:
+        raise SwaError(rc, "swa_attn_kv8_read")
+    return kh, vp
+
+
+def decode_kv8(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_len, window: int = 0, ve=None,
+               gate_x=None, Wg=None, rope_base: float = 1e4, eps: float = 1e-6, *, out=None, lse=None, workspace=None,
+               stream=None, doc_start=None):
+    """One generation step over a paged 8-bit cache (C call swa_attn_kv8_decode), requests of different
+    lengths: q (B,H,D), k, v (B,Hkv,D) bf16 of each request's new token, which is at position seq_len[b] - 1;
+    seq_len int32 (B,) counts it (0: an empty row); block_table int32 (B, max_pages); the cache as for
+    ``kv8_write``, updated in place.  k = v = None: the tokens are in the cache already.
+    ve (B,Hkv,D), gate_x (B,32), Wg [32,Hkv] on value-embedding layers; ``doc_start``: optional int32 (B,),
+    the first position of each request's current document.
+    Returns (out (B,H,D) bf16, lse (B,H) fp32).  Raises SwaError on a nonzero status."""
+    import torch
+    if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q must be (B, H, D), the caches (n_pages, Hkv, page_size, D), block_table (B, max_pages)")
+    B, H, D = q.shape
+    Hkv = k_cache.shape[1]
+    dev = q.device
+    bf = torch.bfloat16
+    _want("q", q, (B, H, D), bf)
+    if (k is None) != (v is None):
+        raise ValueError("k and v go together")
+    if k is not None:
+        _want("k", k, (B, Hkv, D), bf, dev)
+        _want("v", v, (B, Hkv, D), bf, dev)
+    if (ve is None) != (gate_x is None) or (ve is None) != (Wg is None) or (k is None and ve is not None):
+        raise ValueError("ve, gate_x and Wg go together, and with k and v")
+    if ve is not None:
+        _want("ve", ve, (B, Hkv, D), bf, dev)
+        _want("gate_x", gate_x, (B, 32), bf, dev)
+        _want("Wg", Wg, (32, Hkv), bf, dev)
+    n_pages, page_size = _check_kv8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev)
+    max_pages = block_table.shape[1]
+    _want("block_table", block_table, (B, max_pages), torch.int32, dev)
+    _want("seq_len", seq_len, (B,), torch.int32, dev)
+    if doc_start is not None:
+        _want("doc_start", doc_start, (B,), torch.int32, dev)
+    if out is not None:
+        _want("out", out, (B, H, D), bf, dev)
+    if lse is not None:
+        _want("lse", lse, (B, H), torch.float32, dev)
+    if workspace is not None:
+        _want_workspace(workspace, dev)
+    ctx, st = _on_stream(stream, dev)
+    with ctx:
+        if out is None:
+            out = torch.empty((B, H, D), dtype=bf, device=dev)
+        if lse is None:
+            lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+        if workspace is None:
+            need = swa_attn_kv8_decode_workspace_bytes(B, H, Hkv, D)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        rc = swa_attn_kv8_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(ve), _ptr(gate_x), _ptr(Wg), _ptr(k_cache),
+                                 _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_len),
+                                 _ptr(doc_start), _ptr(out), _ptr(lse), B, H, Hkv, D, n_pages, page_size, max_pages,
+                                 int(window), float(rope_base), float(eps), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), st)
+    if rc != SWA_OK:
+        raise SwaError(rc, "swa_attn_kv8_decode")
+    return out, lse
+
+
 def check_device_status(stream=None) -> None:
     """Synchronise and raise SwaError if a kernel recorded an error (e.g. a wait timeout)."""
     rc, detail = swa_attn_last_device_status(_stream_handle(stream))
@@ -574,7 +798,8 @@ def check_device_status(stream=None) -> None:
 
 
 __all__ = [
-    "forward", "decode", "backward", "qkv_prologue", "forward_x", "check_device_status", "SwaError",
+    "forward", "decode", "backward", "qkv_prologue", "forward_x", "kv_pages", "kv8_write", "kv8_read", "decode_kv8",
+    "check_device_status", "SwaError",
     "LIB_PATH", "load", "swa_attn_fwd", "swa_attn_fwd_ws", "swa_attn_fwd_noalloc",
     "swa_attn_noalloc_scratch_bytes", "swa_attn_workspace_bytes", "swa_attn_workspace_offset",
     "swa_attn_rope_table", "swa_attn_prologue", "swa_attn_attention", "swa_attn_strerror",
@@ -584,4 +809,6 @@ __all__ = [
     "swa_attn_bwd", "swa_attn_bwd_saved", "swa_attn_bwd_gqa", "swa_attn_bwd_doc",
     "swa_attn_bwd_workspace_bytes", "swa_attn_fwd_x", "swa_attn_qkv_prologue",
     "swa_attn_fwd_x_workspace_bytes",
+    "swa_attn_kv_pages", "swa_attn_kv8_write", "swa_attn_kv8_read", "swa_attn_kv8_decode",
+    "swa_attn_kv8_decode_workspace_bytes",
 ]

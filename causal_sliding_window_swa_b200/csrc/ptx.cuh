@@ -17,8 +17,11 @@ __device__ unsigned int g_status;
 
 enum : unsigned int {
     kErrTimeout = 5u,     // a bounded wait expired
-    kErrLayout = 6u       // shared memory did not start at the alignment the kernel was built for
+    kErrLayout = 6u,      // shared memory did not start at the alignment the kernel was built for
+    kErrIndex = 7u        // a slot, page or length on the device lies outside the cache (skipped)
 };
+// Sites of kErrIndex: a slot of the slot map, a page of the block table, a sequence length.
+enum : unsigned int { kSiteKvSlot = 80, kSiteKvPage = 81, kSiteKvLen = 82 };
 
 __device__ __forceinline__ void record_error(unsigned int kind, unsigned int site) {
     unsigned int code = (kind & 0xffu) | ((site & 0xffu) << 8) |

@@ -1,7 +1,7 @@
 // swa_attn.cu -- host side of the C ABI declared in include/swa_attn.h: argument checks,
 // workspace management, TMA descriptors and the two kernel launches (prologue, attention).
 // All kernels are in this translation unit (ptx.cuh, prologue.cuh, attn_fwd.cuh, attn_bwd.cuh,
-// decode.cuh).
+// decode.cuh, kv8.cuh, kv8_decode.cuh).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -16,6 +16,8 @@
 #include "attn_bwd.cuh"
 #include "attn_fwd.cuh"
 #include "decode.cuh"
+#include "kv8.cuh"
+#include "kv8_decode.cuh"
 #include "prologue.cuh"
 #include "qkv_gemm.cuh"
 #include "docmask.cuh"
@@ -1253,6 +1255,192 @@ int swa_attn_decode(const void* q, const void* k, const void* v, const void* ve,
                                window, rope_base, eps, workspace, ws_bytes, stream);
 }
 
+// ------------------------------------------------------------- paged 8-bit key/value cache
+
+}  // extern "C"
+
+namespace {
+
+// Page size and page count of a cache: P in {16, 32, 64, 128}, slots (and, given Hkv, the cache's rows)
+// within int32.
+int check_pages(int n_pages, int page_size, int Hkv, int* log_p) {
+    if (n_pages < 1 || Hkv < 1) return SWA_ERR_INVALID_ARG;
+    int lg = 4;
+    while (lg < 8 && (1 << lg) != page_size) ++lg;
+    if (lg == 8) return SWA_ERR_UNSUPPORTED;
+    if ((long long)n_pages * page_size * Hkv >= (1ll << 31)) return SWA_ERR_UNSUPPORTED;
+    *log_p = lg;
+    return SWA_OK;
+}
+
+int check_cache(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale) {
+    if (!k_cache || !v_cache || !k_scale || !v_scale) return SWA_ERR_INVALID_ARG;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return SWA_ERR_MISALIGNED;
+    return SWA_OK;
+}
+
+// Rows (B, T, Hkv, D) of khat and v' and their slots.
+int check_kv8_rows(int B, int T, int Hkv, int D, const void* kh, const void* vp, const int* slots) {
+    if (B < 1 || T < 1 || Hkv < 1) return SWA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return SWA_ERR_UNSUPPORTED;
+    if (Hkv > 65535 || (long long)B * T >= (1ll << 31) || (long long)B * T * Hkv >= (1ll << 31))
+        return SWA_ERR_UNSUPPORTED;
+    if (!kh || !vp || !slots) return SWA_ERR_INVALID_ARG;
+    if (!aligned(kh, 16) || !aligned(vp, 16) || !aligned(slots, 4)) return SWA_ERR_MISALIGNED;
+    return SWA_OK;
+}
+
+template <int D, int IT>
+void launch_kv8_write(const void* kh, const void* vp, const int* slots, const swa::Kv8Store& c, int n_tokens, int win,
+                      cudaStream_t st) {
+    const dim3 grid((unsigned)((n_tokens + (long long)win - 1) / win), (unsigned)c.Hkv);
+    swa::kv8_write_kernel<D, IT><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(kh),
+                                                       static_cast<const __nv_bfloat16*>(vp), slots, c, n_tokens, win);
+}
+
+}  // namespace
+
+extern "C" {
+
+int swa_attn_kv_pages(const int* block_table, const int* kv_len, const int* first_page, const int* pool, const int* n_new,
+                      int* ring, int* block_table_out, int* kv_len_out, int* first_page_out, int* pool_out, int* slots,
+                      int* step_len, int B, int T, int max_pages, int n_pages, int page_size, int window,
+                      swa_stream_t stream) {
+    int log_p;
+    if (B < 1 || T < 1 || max_pages < 1) return SWA_ERR_INVALID_ARG;
+    int rc = check_pages(n_pages, page_size, 1, &log_p);
+    if (rc != SWA_OK) return rc;
+    if ((long long)B * T >= (1ll << 31) || (long long)B * max_pages >= (1ll << 31) ||
+        (long long)max_pages * page_size >= (1ll << 31))
+        return SWA_ERR_UNSUPPORTED;
+    const int* in[5] = {block_table, kv_len, first_page, pool, n_new};
+    int* out[7] = {ring, block_table_out, kv_len_out, first_page_out, pool_out, slots, step_len};
+    for (const int* p : in)
+        if (!p) return SWA_ERR_INVALID_ARG;
+    for (int* p : out)
+        if (!p) return SWA_ERR_INVALID_ARG;
+    for (const int* p : in)
+        if (!aligned(p, 4)) return SWA_ERR_MISALIGNED;
+    for (int* p : out)
+        if (!aligned(p, 4)) return SWA_ERR_MISALIGNED;
+    int dev;
+    if ((rc = device_ready(&dev)) != SWA_OK) return rc;
+    swa::PagesParams p{block_table, kv_len, first_page, pool, n_new, ring, block_table_out, kv_len_out, first_page_out,
+                       pool_out, slots, step_len, B, T, max_pages, n_pages, log_p, std::max(0, window)};
+    swa::kv_pages_kernel<<<1, 1024, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+int swa_attn_kv8_write(const void* kh, const void* vp, const int* slots, void* k_cache, void* v_cache, float* k_scale,
+                       float* v_scale, int B, int T, int Hkv, int D, int n_pages, int page_size, swa_stream_t stream) {
+    int log_p;
+    int rc = check_kv8_rows(B, T, Hkv, D, kh, vp, slots);
+    if (rc == SWA_OK) rc = check_pages(n_pages, page_size, Hkv, &log_p);
+    if (rc == SWA_OK) rc = check_cache(k_cache, v_cache, k_scale, v_scale);
+    if (rc != SWA_OK) return rc;
+    int dev;
+    if ((rc = device_ready(&dev)) != SWA_OK) return rc;
+    const swa::Kv8Store c{static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale, v_scale, n_pages, Hkv,
+                          log_p};
+    const int n_tokens = B * T;
+    const int rows = 256 / (D / 8);
+    // windows of one page; smaller ones while they do not fill the GPU
+    const int win = (long long)(n_tokens / rows) * Hkv <= 8ll * g_num_sms[dev] ? rows : std::max(rows, page_size);
+    const int it = std::max(1, page_size / rows);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (D == 128) {
+        if (it == 1) launch_kv8_write<128, 1>(kh, vp, slots, c, n_tokens, win, st);
+        else if (it == 2) launch_kv8_write<128, 2>(kh, vp, slots, c, n_tokens, win, st);
+        else if (it == 4) launch_kv8_write<128, 4>(kh, vp, slots, c, n_tokens, win, st);
+        else launch_kv8_write<128, 8>(kh, vp, slots, c, n_tokens, win, st);
+    } else {
+        if (it == 1) launch_kv8_write<64, 1>(kh, vp, slots, c, n_tokens, win, st);
+        else if (it == 2) launch_kv8_write<64, 2>(kh, vp, slots, c, n_tokens, win, st);
+        else launch_kv8_write<64, 4>(kh, vp, slots, c, n_tokens, win, st);
+    }
+    return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+int swa_attn_kv8_read(const int* slots, const void* k_cache, const void* v_cache, const float* k_scale,
+                      const float* v_scale, void* kh, void* vp, int B, int T, int Hkv, int D, int n_pages, int page_size,
+                      swa_stream_t stream) {
+    int log_p;
+    int rc = check_kv8_rows(B, T, Hkv, D, kh, vp, slots);
+    if (rc == SWA_OK) rc = check_pages(n_pages, page_size, Hkv, &log_p);
+    if (rc == SWA_OK) rc = check_cache(k_cache, v_cache, k_scale, v_scale);
+    if (rc != SWA_OK) return rc;
+    int dev;
+    if ((rc = device_ready(&dev)) != SWA_OK) return rc;
+    const swa::Kv8Store c{static_cast<uint8_t*>(const_cast<void*>(k_cache)), static_cast<uint8_t*>(const_cast<void*>(v_cache)),
+                          const_cast<float*>(k_scale), const_cast<float*>(v_scale), n_pages, Hkv, log_p};
+    const int n_rows = B * T * Hkv;
+    const long long blocks = std::min<long long>(((long long)n_rows * (D / 8) + 255) / 256, 148ll * 64);
+    const swa::FastDiv divH = make_fastdiv(Hkv);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    __nv_bfloat16 *kp = static_cast<__nv_bfloat16*>(kh), *vpp = static_cast<__nv_bfloat16*>(vp);
+    if (D == 128)
+        swa::kv8_read_kernel<128><<<(unsigned)blocks, 256, 0, st>>>(slots, c, kp, vpp, n_rows, divH);
+    else
+        swa::kv8_read_kernel<64><<<(unsigned)blocks, 256, 0, st>>>(slots, c, kp, vpp, n_rows, divH);
+    return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+// Workspace: qhat of the new tokens (B*H*D bf16), 1024-byte aligned.
+size_t swa_attn_kv8_decode_workspace_bytes(int B, int H, int Hkv, int D) {
+    Shape s;
+    if (check_sizes(B, 1, H, D, &s) != SWA_OK || check_kv_heads(Hkv, &s) != SWA_OK || H / Hkv > swa::kKv8MaxGroup)
+        return 0;
+    return round_up((size_t)s.n * 2);
+}
+
+int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void* ve, const void* gate_x, const void* Wg,
+                        void* k_cache, void* v_cache, float* k_scale, float* v_scale, const int* block_table,
+                        const int* seq_len, const int* doc_start, void* out, float* lse, int B, int H, int Hkv, int D,
+                        int n_pages, int page_size, int max_pages, int window, float rope_base, float eps, void* workspace,
+                        size_t ws_bytes, swa_stream_t stream) {
+    Shape s;
+    int log_p;
+    int rc = check_sizes(B, 1, H, D, &s);
+    if (rc == SWA_OK) rc = check_kv_heads(Hkv, &s);
+    if (rc != SWA_OK) return rc;
+    if (H / Hkv > swa::kKv8MaxGroup) return SWA_ERR_UNSUPPORTED;
+    // without a new token there is no value embedding either
+    if ((k == nullptr) != (v == nullptr) || (k == nullptr && (ve || gate_x || Wg))) return SWA_ERR_INVALID_ARG;
+    rc = check_layer_args(q, k ? k : q, v ? v : q, ve, gate_x, Wg, rope_base, eps);
+    if (rc == SWA_OK) rc = check_outputs(out, lse);
+    if (rc == SWA_OK) rc = check_pages(n_pages, page_size, Hkv, &log_p);
+    if (rc == SWA_OK) rc = check_cache(k_cache, v_cache, k_scale, v_scale);
+    if (rc != SWA_OK) return rc;
+    if (!block_table || !seq_len || !workspace || max_pages < 1) return SWA_ERR_INVALID_ARG;
+    if ((long long)max_pages * page_size >= (1ll << 31)) return SWA_ERR_UNSUPPORTED;
+    if (!aligned(block_table, 4) || !aligned(seq_len, 4) || (doc_start && !aligned(doc_start, 4)) || !aligned(workspace, 16))
+        return SWA_ERR_MISALIGNED;
+    if (ws_bytes < swa_attn_kv8_decode_workspace_bytes(B, H, Hkv, D)) return SWA_ERR_NO_MEMORY;
+    int dev;
+    if ((rc = device_ready(&dev)) != SWA_OK) return rc;
+    using bf = __nv_bfloat16;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const swa::Kv8Store c{static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale, v_scale, n_pages, Hkv,
+                          log_p};
+    swa::Kv8TokenParams t{static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v),
+                          static_cast<const bf*>(ve), static_cast<const bf*>(gate_x), static_cast<const bf*>(Wg),
+                          block_table, seq_len, static_cast<bf*>(workspace), static_cast<bf*>(out), lse, c, H, max_pages,
+                          (double)rope_base, (double)eps};
+    const int rows = 256 / (D / 8);
+    const dim3 tg((unsigned)B, (unsigned)((H + (k ? Hkv : 0) + rows - 1) / rows));
+    swa::Kv8AttnParams a{static_cast<const bf*>(workspace), block_table, seq_len, doc_start, static_cast<bf*>(out), lse, c, H,
+                         H / Hkv, max_pages, std::max(0, window), (float)(1.4426950408889634 / std::sqrt((double)D))};
+    if (D == 128) {
+        swa::kv8_token_kernel<128><<<tg, 256, 0, st>>>(t);
+        swa::kv8_attn_kernel<128><<<(unsigned)(B * H), 128, 0, st>>>(a);
+    } else {
+        swa::kv8_token_kernel<64><<<tg, 256, 0, st>>>(t);
+        swa::kv8_attn_kernel<64><<<(unsigned)(B * H), 128, 0, st>>>(a);
+    }
+    return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
 int swa_attn_selftest_wait(int limit_ms, swa_stream_t stream) {
     if (limit_ms < 1 || limit_ms > 10000) return SWA_ERR_INVALID_ARG;
     int dev;
@@ -1277,6 +1465,7 @@ int swa_attn_last_device_status(swa_stream_t stream, unsigned int* detail) {
     }
     if (detail) *detail = word;
     if (word == 0) return SWA_OK;
+    if ((word & 0xffu) == swa::kErrIndex) return SWA_ERR_INVALID_ARG;
     return (word & 0xffu) == swa::kErrTimeout ? SWA_ERR_TIMEOUT : SWA_ERR_CUDA;
 }
 

@@ -66,7 +66,8 @@ typedef struct CUstream_st* swa_stream_t;
 
 typedef enum swa_status {
     SWA_OK = 0,
-    SWA_ERR_INVALID_ARG = -1,  /* null pointer, size < 1, bad eps / rope_base, ve/gate_x/Wg partly set */
+    SWA_ERR_INVALID_ARG = -1,  /* null pointer, size < 1, bad eps / rope_base, ve/gate_x/Wg partly set, or
+                                  (read via last_device_status) a slot, page or length outside a paged cache */
     SWA_ERR_UNSUPPORTED = -2,  /* D not in {64, 128}, sizes beyond int32 indexing, device not sm_100 */
     SWA_ERR_MISALIGNED = -3,   /* a tensor pointer or the workspace is not 16-byte aligned */
     SWA_ERR_CUDA = -4,         /* a CUDA runtime / driver call failed (launch, allocation by CUDA),
@@ -232,8 +233,9 @@ SWA_API const char* swa_attn_strerror(int status);
 
 /*
  * Synchronises `stream`, then returns and clears the current device's status word:
- * SWA_OK, SWA_ERR_TIMEOUT (a bounded wait expired in some kernel since the last read) or
- * SWA_ERR_CUDA (the stream reported an error).  If `detail` is not NULL it receives the raw
+ * SWA_OK, SWA_ERR_TIMEOUT (a bounded wait expired in some kernel since the last read),
+ * SWA_ERR_INVALID_ARG (a kernel of the paged cache met a slot, page or length outside it and skipped
+ * it) or SWA_ERR_CUDA (the stream reported an error).  If `detail` is not NULL it receives the raw
  * word (bits 0-7 kind, 8-15 wait site, 16-31 block index).
  */
 SWA_API int swa_attn_last_device_status(swa_stream_t stream, unsigned int* detail);
@@ -406,6 +408,111 @@ SWA_API int swa_attn_bwd(const void* q, const void* k, const void* v, const void
                          float* dgate_x, float* dWg, int B, int T, int H, int D, int window,
                          float rope_base, float eps, void* workspace, size_t ws_bytes,
                          swa_stream_t stream);
+
+/*
+ * A paged key/value cache in 8 bits, for decoding requests of different lengths (the pages list a KV
+ * cache among the missing pieces: "Let's reproduce GPT-2 (124M)" notes, section 19).
+ *
+ * The cache.  P = page_size tokens of every key/value head make a page, P in {16, 32, 64, 128}:
+ *   k_cache, v_cache  e4m3 (n_pages, Hkv, P, D): khat and v' as codes; a value is code * scale.
+ *   k_scale, v_scale  fp32 (n_pages, Hkv): one scale for each page and head, a power of two 2^e, e the
+ *                     smallest integer >= -60 with max |value| <= 448 * 2^e over the page's tokens.
+ * Caller-owned, 16-byte (scales: 4-byte) aligned; n_pages * Hkv * P < 2^31.  Slot s of a cache is token
+ * s % P of page s / P.  Nothing has to be initialised: a page's scale starts anew with its token 0.
+ * While a page fills, its scale grows where a new token needs it, and the codes already there are moved
+ * to the new scale: exactly, but for values below 2^-14 of the page's largest, which are rounded again.
+ * Caching rounds a value to 4 significant bits (half a step is 2^-4 of it, or 2^-10 of the scale).
+ * An infinity becomes the largest code at the largest scale, 2^120; a NaN stays a NaN and does not
+ * count towards the scale.
+ *
+ * Requests.  Row b of block_table, int32 (B, max_pages), lists request b's pages in token order: token
+ * at position x is in page block_table[b, x / P].  Entries of pages not held are -1.
+ *
+ * swa_attn_kv_pages: one step of the page allocator, on the GPU, from the requests' lengths.
+ *   kv_len      int32 (B): tokens each request has in the cache.
+ *   first_page  int32 (B): its pages before this one were given back (0 for a new request).
+ *   n_new       int32 (B): tokens that join it in this step, 0 .. T; 0 leaves it idle; negative: it has
+ *               ended, gives back all its pages and is empty afterwards.
+ *   pool        int32 (2): {head, free}; ring  int32 (n_pages): the free pages are
+ *               ring[(head + i) % n_pages], i < free.  A new cache has ring = 0 .. n_pages - 1, pool = {0, n_pages}.
+ * With L = kv_len[b], n = n_new[b]:
+ *   window > 0: pages that no later query of that window can see, entries before
+ *     max(0, L - window + 1) / P, go back to the ring (a cache for several layers: the largest window;
+ *     window <= 0: all pages are kept);
+ *   need_b = ceil((L + n) / P) - ceil(L / P) pages are taken.  Request b is served iff n >= 1 and either
+ *     need_b = 0 or the sum of need over requests 0 .. b is at most `free`: requests are served in order, one that
+ *     finds no page holds back those after it that need one, and pages given back in a step are free from the
+ *     next step on.  A request that cannot be served at all (n > T, more than max_pages pages, or a
+ *     kv_len or first_page that is not possible) is left as it was and holds nobody back.
+ * Results (each may be the array it follows from, for a step in place; other overlaps are not allowed):
+ *   block_table_out, kv_len_out, first_page_out, pool_out   the state after the step (ring is always updated in
+ *               place: only entries outside the free stretch change, so a step can be repeated from
+ *               the same inputs);
+ *   slots       int32 (B, T): slots[b, t] is the slot of request b's t-th new token, -1 for t >= n_new[b] and
+ *               for requests that were not served;
+ *   step_len    int32 (B): kv_len_out[b] where tokens joined, else 0: the seq_len of swa_attn_kv8_decode.
+ *               A request that asked for tokens and has step_len 0 was not served.
+ * Errors: SWA_ERR_INVALID_ARG (null pointer, size < 1), SWA_ERR_UNSUPPORTED (page_size, n_pages * page_size,
+ * max_pages * page_size, B * T or B * max_pages at least 2^31), SWA_ERR_MISALIGNED (4 bytes), SWA_ERR_CUDA.
+ */
+SWA_API int swa_attn_kv_pages(const int* block_table, const int* kv_len, const int* first_page, const int* pool,
+                              const int* n_new, int* ring, int* block_table_out, int* kv_len_out,
+                              int* first_page_out, int* pool_out, int* slots, int* step_len, int B, int T,
+                              int max_pages, int n_pages, int page_size, int window, swa_stream_t stream);
+
+/*
+ * swa_attn_kv8_write: rows kh, vp bf16 (B, T, Hkv, D) (khat and v', as swa_attn_qkv_prologue or the workspace
+ * of swa_attn_fwd_ws gives them for positions 0, 1, ...) into the slots of slots, int32 (B, T).  Rows whose
+ * slot is negative are skipped; a slot past the cache is recorded (swa_attn_last_device_status) and
+ * skipped.  The rows of one call that go into one page must follow one another in row order and in the
+ * page (as swa_attn_kv_pages numbers them), and no slot may appear twice: otherwise that page's values are
+ * unspecified.  Tokens of a page before the first slot written there must be in the cache already, unless
+ * that is the page's token 0.  Nothing but the pages and scales of the slots is written.
+ * Errors: SWA_ERR_INVALID_ARG, SWA_ERR_UNSUPPORTED (D not 64 / 128, page_size, n_pages * Hkv * page_size or
+ * B * T * Hkv at least 2^31, Hkv > 65535), SWA_ERR_MISALIGNED, SWA_ERR_CUDA.
+ */
+SWA_API int swa_attn_kv8_write(const void* kh, const void* vp, const int* slots, void* k_cache, void* v_cache,
+                               float* k_scale, float* v_scale, int B, int T, int Hkv, int D, int n_pages,
+                               int page_size, swa_stream_t stream);
+
+/*
+ * swa_attn_kv8_read: the reverse, kh, vp bf16 (B, T, Hkv, D) = code * scale of the given slots, exact (for
+ * a request that is moved: what is read here and written to other pages keeps its values).  Slots may
+ * repeat.  Rows with a negative slot, or one past the cache (recorded), are zeros.  Errors as
+ * swa_attn_kv8_write.
+ */
+SWA_API int swa_attn_kv8_read(const int* slots, const void* k_cache, const void* v_cache, const float* k_scale,
+                              const float* v_scale, void* kh, void* vp, int B, int T, int Hkv, int D,
+                              int n_pages, int page_size, swa_stream_t stream);
+
+/*
+ * swa_attn_kv8_decode: one generation step over the paged cache, as swa_attn_decode_doc with a length for
+ * each request.  Request b has n_b = seq_len[b] tokens, its new one at position n_b - 1:
+ *   1. the prologue of swa_attn_decode at that position; khat and v' go into its slot (as
+ *      swa_attn_kv8_write).  k = v = NULL: the token is in the cache already, only q is used (then
+ *      ve, gate_x, Wg are NULL too).
+ *   2. out[b,h,:] = sum_j softmax_j(qhat . k_j / sqrt(D)) v_j over the cached keys j in
+ *      [max(0, n_b - window, min(doc_start[b], n_b - 1)), n_b) (window <= 0: no window; doc_start int32 (B) or
+ *      NULL), lse[b,h] = ln sum_j exp(qhat . k_j / sqrt(D)); query head h reads key/value head
+ *      h / (H / Hkv).  Entries of the block table before the first of these keys are not read.
+ *   Requests with seq_len <= 0 are empty rows: out = 0, lse = -inf, the cache is left alone.
+ *   q, out bf16 (B, H, D); k, v, ve bf16 (B, Hkv, D); gate_x bf16 (B, 32); Wg bf16 [32, Hkv]; lse fp32 (B, H) or NULL;
+ *   block_table int32 (B, max_pages); seq_len int32 (B).  Two requests may share pages, but not the page
+ *   that takes a new token.  workspace: swa_attn_kv8_decode_workspace_bytes() bytes, 16-byte aligned,
+ *   nothing kept between calls; calls that may overlap need one each.
+ * A seq_len beyond max_pages * page_size (an empty row) and pages outside the cache (their keys are not
+ * visible, a token that belongs there is not stored) are recorded: swa_attn_last_device_status.
+ * Scores, exponentials and sums are fp32; the weights enter the products with v_j rounded to 11 bits.
+ * Errors: SWA_ERR_INVALID_ARG, SWA_ERR_UNSUPPORTED (D not 64 / 128, page_size, H / Hkv > 64, sizes beyond int32),
+ * SWA_ERR_MISALIGNED, SWA_ERR_NO_MEMORY (workspace too small), SWA_ERR_CUDA.
+ */
+SWA_API size_t swa_attn_kv8_decode_workspace_bytes(int B, int H, int Hkv, int D);
+SWA_API int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void* ve, const void* gate_x,
+                                const void* Wg, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                const int* block_table, const int* seq_len, const int* doc_start, void* out,
+                                float* lse, int B, int H, int Hkv, int D, int n_pages, int page_size,
+                                int max_pages, int window, float rope_base, float eps, void* workspace,
+                                size_t ws_bytes, swa_stream_t stream);
 
 /*
  * Failure-detection self-test (no counterpart in the pages).  Enqueues on `stream` one block of
