@@ -32,15 +32,6 @@
 
 namespace swa {
 
-// 2-D tiled load of one box into shared memory, completing its bytes on the mbarrier.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-}
-
 template <int BN>
 struct QkvCfg {
     static constexpr int BM = 128;                       // tokens per tile (MMA M)

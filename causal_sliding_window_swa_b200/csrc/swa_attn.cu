@@ -1386,12 +1386,82 @@ int swa_attn_kv8_read(const int* slots, const void* k_cache, const void* v_cache
     return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
-// Workspace: qhat of the new tokens (B*H*D bf16), 1024-byte aligned.
+}  // extern "C"
+
+namespace {
+
+// qhat of the new tokens | arrival counters | results of the pieces of shared items, two for each block of the
+// attention kernel; each section 1024-byte aligned.
+struct Kv8DecLayout {
+    size_t qh, counters, part, total;
+};
+Kv8DecLayout kv8_dec_layout(const Shape& s) {
+    Kv8DecLayout w{};
+    w.counters = round_up((size_t)s.n * 2);
+    w.part = w.counters + round_up(swa::kKv8MaxBlocks * sizeof(int));
+    w.total = w.part + round_up((size_t)2 * swa::kKv8MaxBlocks * (s.H / s.Hkv) * (s.D + 4) * sizeof(float));
+    return w;
+}
+
+int check_kv8_heads(int B, int H, int Hkv, int D, Shape* s) {
+    int rc = check_sizes(B, 1, H, D, s);
+    if (rc == SWA_OK) rc = check_kv_heads(Hkv, s);
+    if (rc == SWA_OK && H / Hkv > swa::kKv8MaxGroup) rc = SWA_ERR_UNSUPPORTED;
+    return rc;
+}
+
+// The pages as {D, n_pages * Hkv * P} bytes; box = one page of one head.
+bool make_page_map(CUtensorMap* m, const void* base, long long rows, int D, int P) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)D};
+    const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)P};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NRT>
+bool set_kv8_smem() {
+    return cudaFuncSetAttribute(swa::kv8_attn_kernel<D, NRT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                swa::Kv8Cfg<D>::SMEM) == cudaSuccess;
+}
+
+template <int D>
+int launch_kv8_attention(int dev, const swa::Kv8AttnParams& a, cudaStream_t st) {
+    using C = swa::Kv8Cfg<D>;
+    {
+        static std::once_flag once[64];
+        static bool ok[64] = {false};
+        std::call_once(once[dev], [&] {
+            ok[dev] = set_kv8_smem<D, 1>() && set_kv8_smem<D, 2>() && set_kv8_smem<D, 4>() && set_kv8_smem<D, 8>();
+        });
+        if (!ok[dev]) {
+            cudaGetLastError();
+            return SWA_ERR_CUDA;
+        }
+    }
+    CUtensorMap tk, tv;
+    const long long rows = ((long long)a.c.n_pages * a.c.Hkv) << a.c.log_p;
+    if (!make_page_map(&tk, a.c.k_cache, rows, D, 1 << a.c.log_p) || !make_page_map(&tv, a.c.v_cache, rows, D, 1 << a.c.log_p))
+        return SWA_ERR_CUDA;
+    const dim3 grid((unsigned)std::min(g_num_sms[dev], swa::kKv8MaxBlocks)), block(C::THREADS);
+    if (a.G <= 8) launch_pdl(swa::kv8_attn_kernel<D, 1>, grid, block, C::SMEM, st, tk, tv, a);
+    else if (a.G <= 16) launch_pdl(swa::kv8_attn_kernel<D, 2>, grid, block, C::SMEM, st, tk, tv, a);
+    else if (a.G <= 32) launch_pdl(swa::kv8_attn_kernel<D, 4>, grid, block, C::SMEM, st, tk, tv, a);
+    else launch_pdl(swa::kv8_attn_kernel<D, 8>, grid, block, C::SMEM, st, tk, tv, a);
+    return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t swa_attn_kv8_decode_workspace_bytes(int B, int H, int Hkv, int D) {
     Shape s;
-    if (check_sizes(B, 1, H, D, &s) != SWA_OK || check_kv_heads(Hkv, &s) != SWA_OK || H / Hkv > swa::kKv8MaxGroup)
-        return 0;
-    return round_up((size_t)s.n * 2);
+    return check_kv8_heads(B, H, Hkv, D, &s) == SWA_OK ? kv8_dec_layout(s).total : 0;
 }
 
 int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void* ve, const void* gate_x, const void* Wg,
@@ -1401,10 +1471,8 @@ int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void*
                         size_t ws_bytes, swa_stream_t stream) {
     Shape s;
     int log_p;
-    int rc = check_sizes(B, 1, H, D, &s);
-    if (rc == SWA_OK) rc = check_kv_heads(Hkv, &s);
+    int rc = check_kv8_heads(B, H, Hkv, D, &s);
     if (rc != SWA_OK) return rc;
-    if (H / Hkv > swa::kKv8MaxGroup) return SWA_ERR_UNSUPPORTED;
     // without a new token there is no value embedding either
     if ((k == nullptr) != (v == nullptr) || (k == nullptr && (ve || gate_x || Wg))) return SWA_ERR_INVALID_ARG;
     rc = check_layer_args(q, k ? k : q, v ? v : q, ve, gate_x, Wg, rope_base, eps);
@@ -1416,29 +1484,28 @@ int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void*
     if ((long long)max_pages * page_size >= (1ll << 31)) return SWA_ERR_UNSUPPORTED;
     if (!aligned(block_table, 4) || !aligned(seq_len, 4) || (doc_start && !aligned(doc_start, 4)) || !aligned(workspace, 16))
         return SWA_ERR_MISALIGNED;
-    if (ws_bytes < swa_attn_kv8_decode_workspace_bytes(B, H, Hkv, D)) return SWA_ERR_NO_MEMORY;
+    const Kv8DecLayout L = kv8_dec_layout(s);
+    if (ws_bytes < L.total) return SWA_ERR_NO_MEMORY;
     int dev;
     if ((rc = device_ready(&dev)) != SWA_OK) return rc;
     using bf = __nv_bfloat16;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const swa::Kv8Store c{static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale, v_scale, n_pages, Hkv,
                           log_p};
-    swa::Kv8TokenParams t{static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v),
-                          static_cast<const bf*>(ve), static_cast<const bf*>(gate_x), static_cast<const bf*>(Wg),
-                          block_table, seq_len, static_cast<bf*>(workspace), static_cast<bf*>(out), lse, c, H, max_pages,
-                          (double)rope_base, (double)eps};
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int* counters = reinterpret_cast<int*>(ws + L.counters);
+    const swa::Kv8TokenParams t{static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v),
+                                static_cast<const bf*>(ve), static_cast<const bf*>(gate_x), static_cast<const bf*>(Wg),
+                                block_table, seq_len, reinterpret_cast<bf*>(ws + L.qh), static_cast<bf*>(out), lse, c, H,
+                                max_pages, counters, swa::kKv8MaxBlocks, (double)rope_base, (double)eps};
     const int rows = 256 / (D / 8);
     const dim3 tg((unsigned)B, (unsigned)((H + (k ? Hkv : 0) + rows - 1) / rows));
-    swa::Kv8AttnParams a{static_cast<const bf*>(workspace), block_table, seq_len, doc_start, static_cast<bf*>(out), lse, c, H,
-                         H / Hkv, max_pages, std::max(0, window), (float)(1.4426950408889634 / std::sqrt((double)D))};
-    if (D == 128) {
-        swa::kv8_token_kernel<128><<<tg, 256, 0, st>>>(t);
-        swa::kv8_attn_kernel<128><<<(unsigned)(B * H), 128, 0, st>>>(a);
-    } else {
-        swa::kv8_token_kernel<64><<<tg, 256, 0, st>>>(t);
-        swa::kv8_attn_kernel<64><<<(unsigned)(B * H), 128, 0, st>>>(a);
-    }
-    return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+    const swa::Kv8AttnParams a{reinterpret_cast<const bf*>(ws + L.qh), block_table, seq_len, doc_start, static_cast<bf*>(out),
+                               lse, c, counters, reinterpret_cast<float*>(ws + L.part), B, H, H / Hkv, max_pages,
+                               std::max(0, window), (float)(1.4426950408889634 / std::sqrt((double)D)), wait_limit_ns()};
+    if (D == 128) swa::kv8_token_kernel<128><<<tg, 256, 0, st>>>(t);
+    else swa::kv8_token_kernel<64><<<tg, 256, 0, st>>>(t);
+    return D == 128 ? launch_kv8_attention<128>(dev, a, st) : launch_kv8_attention<64>(dev, a, st);
 }
 
 int swa_attn_selftest_wait(int limit_ms, swa_stream_t stream) {
