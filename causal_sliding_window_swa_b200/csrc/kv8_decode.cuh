@@ -191,8 +191,11 @@ __global__ void __launch_bounds__(256) kv8_token_kernel(const Kv8TokenParams p) 
 // weight, an eighth of the output's own rounding).  m is raised, with one rescaling, only when some
 // x_j + log2(value scale) passes it by more than 2^kSlack: it is at least the first tile's maximum, so
 // weights stay below 2^kSlack and those that fp16 loses are below 2^-24 of the largest.
-constexpr int kKv8Chunk = 128;          // key positions of a unit
-constexpr int kKv8MaxBlocks = 148;      // blocks of the attention kernel, at most
+constexpr int kKv8Chunk = 64;           // key positions of a unit
+constexpr int kKv8Tiles = kKv8Chunk / 16;
+constexpr int kKv8Sms = 148;
+// Blocks of the attention kernel, at most: two per SM where a warp has one group of eight heads, else one.
+__host__ __device__ constexpr int kv8_max_blocks(int G) { return G <= 8 ? 2 * kKv8Sms : kKv8Sms; }
 constexpr float kSlack = 10.f;          // fp16 holds 2^15
 
 enum : unsigned int { kSiteKv8Full = 83, kSiteKv8Empty = 84 };
@@ -212,17 +215,30 @@ struct Kv8AttnParams {
     unsigned long long wait_limit_ns;
 };
 
-template <int D>
+// NT groups of eight query heads per warp; NRG sets of warps that split more groups than that.
+template <int D, int NT, int NRG>
 struct Kv8Cfg {
     static constexpr int CONSUMERS = 8;
     static constexpr int THREADS = 32 * (CONSUMERS + 1);
+    static constexpr int BLOCKS_PER_SM = NT == 1 ? 2 : 1;
+    static constexpr int KSLOTS = CONSUMERS / NRG;               // warps that share the keys of a group of heads
+    static constexpr int SETS = KSLOTS / kKv8Tiles;              // chunks in work at a time
     static constexpr int TENSOR = kKv8Chunk * D;                 // bytes of a chunk's K (and V)
-    static constexpr int NS = D == 128 ? 5 : 8;                  // ring stages
-    static constexpr int OFF_O = NS * 2 * TENSOR;                // warp results [8][8][D]
-    static constexpr int OFF_ML = OFF_O + CONSUMERS * 8 * D * 4; // m [8][8], l [8][8]
-    static constexpr int OFF_META = OFF_ML + 2 * CONSUMERS * 8 * 4;   // per stage and tile: ks c1, vs, log2 vs, pad
-    static constexpr int OFF_BAR = OFF_META + NS * 8 * 16;
+    static constexpr int HEADS = 8 * NT;                         // query heads of a warp
+    // results of half of the warps (the other half's are added in registers first)
+    static constexpr int MERGE = CONSUMERS / 2 * HEADS * D * 4;
+    // Ring stages; a multiple of SETS, so that a set of warps takes every use of its stages and its waits see each
+    // phase of their barriers in turn.
+    static constexpr int NS = NT == 1 ? (D == 128 ? 4 : 10) : (D == 128 ? 8 : 12);
+    static constexpr int OFF_O = NS * 2 * TENSOR;
+    static constexpr int OFF_ML = OFF_O + MERGE;                 // m [8][HEADS], l [8][HEADS]
+    static constexpr int NTG = NT * NRG;                         // groups of eight heads
+    static constexpr int OFF_Q = OFF_ML + 2 * CONSUMERS * HEADS * 4;      // qhat as fp16 operands
+    static constexpr int OFF_META = OFF_Q + NTG * 8 * D * 2;     // per stage and tile: ks c1, vs, log2 vs, pad
+    static constexpr int OFF_BAR = OFF_META + NS * kKv8Tiles * 16;
     static constexpr int SMEM = OFF_BAR + 2 * NS * 8 + 1024;     // + alignment slack
+    static_assert(NS % SETS == 0, "a stage belongs to one set of warps");
+    static_assert(BLOCKS_PER_SM * (SMEM + 2048) <= 228 * 1024, "shared memory");
 };
 
 // First visible key of a request of n tokens.
@@ -237,7 +253,7 @@ struct Kv8Walk {
     int b, hk;             // item
     int n, lo;             // its visible keys [lo, n)
     int ch0, nch;          // its chunks [ch0, ch0 + nch)
-    long long begin;       // its first unit
+    int begin;             // its first unit
 
     __device__ __forceinline__ void load(const Kv8AttnParams& p) {
         n = kv8_length(p.seq_len, b, p.max_pages, p.c.log_p);
@@ -258,7 +274,8 @@ struct Kv8Walk {
 };
 
 // The block that has unit u of n units shared by m blocks: block c has [n c / m, n (c + 1) / m).
-__device__ __forceinline__ int kv8_owner(long long u, long long n, int m) { return (int)(((u + 1) * m - 1) / n); }
+__device__ __forceinline__ int kv8_owner(int u, int n, int m) { return (int)((((unsigned long long)u + 1) * m - 1) / (unsigned)n); }
+__device__ __forceinline__ int kv8_first_unit(int c, int n, int m) { return (int)((unsigned long long)n * c / (unsigned)m); }
 
 __device__ __forceinline__ uint32_t fp8x2_to_half2(uint32_t two) {
     uint32_t r;
@@ -281,35 +298,159 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// What a partial sum (m, l) is multiplied with when the reference becomes M: nothing at all where it is empty.
+__device__ __forceinline__ float kv8_factor(float m, float l, float M) {
+    return m == -INFINITY && l == 0.f ? 0.f : ex2_approx(m - M);
+}
+
+// One tile of 16 keys at position pos0, rows at kr (and `tensor` bytes behind it the values), for NT groups of eight
+// heads.  meta: key scale times c1, value scale, its log2.  q: this lane's qhat operands, two steps in each 16 bytes.
+template <int D, int NT>
+__device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0, int lo, int n, const float4& meta,
+                                         const uint4* q, float (&o)[NT][D / 16][4], float (&m)[NT][2],
+                                         float (&l)[NT][2], int g, int t) {
+    constexpr int NSTEP = D / 16, VW = D / 32;
+    const bool whole = pos0 >= lo && pos0 + 16 <= n;
+    const uint8_t* vr = kr + tensor;
+    uint32_t a[2][NSTEP];                                  // rows g, g + 8
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+            const int row = g + 8 * r;
+            const int at = D == 128 ? row * 128 + (((2 * t + x) ^ (row & 7)) << 4) : row * 64 + ((t ^ ((row >> 1) & 3)) << 4);
+            const uint4 v4 = *reinterpret_cast<const uint4*>(kr + at);
+            a[r][4 * x] = v4.x;
+            a[r][4 * x + 1] = v4.y;
+            a[r][4 * x + 2] = v4.z;
+            a[r][4 * x + 3] = v4.w;
+        }
+    // S^T, in two chains where there is one group
+    constexpr int NC = NT == 1 ? 2 : 1;
+    float sc[NT][NC][4];
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4 * NC; ++e) sc[x][e / 4][e % 4] = 0.f;
+    uint4 qs[NT];
+#pragma unroll
+    for (int st = 0; st < NSTEP; ++st) {
+        if ((st & 1) == 0)
+#pragma unroll
+            for (int x = 0; x < NT; ++x) qs[x] = q[(x * (NSTEP / 2) + st / 2) * 32];
+        const uint32_t a0 = fp8x2_to_half2(a[0][st]), a1 = fp8x2_to_half2(a[1][st]);
+        const uint32_t a2 = fp8x2_to_half2(a[0][st] >> 16), a3 = fp8x2_to_half2(a[1][st] >> 16);
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+            mma_16816(sc[x][st % NC], a0, a1, a2, a3, (st & 1) ? qs[x].z : qs[x].x, (st & 1) ? qs[x].w : qs[x].y);
+    }
+    uint32_t b[NT][2];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+        float s[4];                                        // keys g and g + 8, heads 2 t and 2 t + 1
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = (NC == 2 ? sc[x][0][e] + sc[x][NC - 1][e] : sc[x][0][e]) * meta.x;
+        if (!whole) {
+            if (pos0 + g < lo || pos0 + g >= n) s[0] = s[1] = -INFINITY;
+            if (pos0 + g + 8 < lo || pos0 + g + 8 >= n) s[2] = s[3] = -INFINITY;
+        }
+        float t0 = fmaxf(s[0], s[2]) + meta.z, t1 = fmaxf(s[1], s[3]) + meta.z;
+        if (__any_sync(0xffffffffu, t0 > m[x][0] + kSlack || t1 > m[x][1] + kSlack)) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
+                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
+            }
+            t0 = fmaxf(t0, m[x][0]);
+            t1 = fmaxf(t1, m[x][1]);
+            const float f0 = ex2_approx(m[x][0] - t0), f1 = ex2_approx(m[x][1] - t1);
+            m[x][0] = t0;
+            m[x][1] = t1;
+            l[x][0] *= f0;
+            l[x][1] *= f1;
+#pragma unroll
+            for (int k = 0; k < 2 * VW; ++k) {
+                o[x][k][0] *= f0;
+                o[x][k][1] *= f1;
+                o[x][k][2] *= f0;
+                o[x][k][3] *= f1;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = ex2_approx(s[e] - m[x][e & 1]);
+        l[x][0] += s[0] + s[2];
+        l[x][1] += s[1] + s[3];
+        b[x][0] = movmatrix_trans(pack_half2(s[0] * meta.y, s[1] * meta.y));
+        b[x][1] = movmatrix_trans(pack_half2(s[2] * meta.y, s[3] * meta.y));
+    }
+    uint32_t v[4][VW];                                     // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int row = 2 * t + (x & 1) + 8 * (x >> 1);
+        if (D == 128) {
+            const uint4 v4 = *reinterpret_cast<const uint4*>(vr + row * 128 + ((g ^ (row & 7)) << 4));
+            v[x][0] = v4.x;
+            v[x][1] = v4.y;
+            v[x][VW - 2] = v4.z;
+            v[x][VW - 1] = v4.w;
+        } else {
+            const uint2 v2 = *reinterpret_cast<const uint2*>(vr + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (g & 1));
+            v[x][0] = v2.x;
+            v[x][1] = v2.y;
+        }
+    }
+    if (!whole) {
+        // values of keys outside [lo, n) count for nothing, whatever the page holds there
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int key = pos0 + 2 * t + (x & 1) + 8 * (x >> 1);
+            if (key < lo || key >= n)
+#pragma unroll
+                for (int k = 0; k < VW; ++k) v[x][k] = 0u;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < VW; ++k) {
+        // features 4 k .. 4 k + 3 of this lane, keys (2 t, 2 t + 1) and (2 t + 8, 2 t + 9)
+        const uint32_t p0 = __byte_perm(v[0][k], v[1][k], 0x5140), p1 = __byte_perm(v[2][k], v[3][k], 0x5140);
+        const uint32_t r0 = __byte_perm(v[0][k], v[1][k], 0x7362), r1 = __byte_perm(v[2][k], v[3][k], 0x7362);
+        const uint32_t a0 = fp8x2_to_half2(p0), a1 = fp8x2_to_half2(p0 >> 16), a2 = fp8x2_to_half2(p1), a3 = fp8x2_to_half2(p1 >> 16);
+        const uint32_t c0 = fp8x2_to_half2(r0), c1 = fp8x2_to_half2(r0 >> 16), c2 = fp8x2_to_half2(r1), c3 = fp8x2_to_half2(r1 >> 16);
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            mma_16816(o[x][2 * k], a0, a1, a2, a3, b[x][0], b[x][1]);
+            mma_16816(o[x][2 * k + 1], c0, c1, c2, c3, b[x][0], b[x][1]);
+        }
+    }
+}
+
 __device__ __forceinline__ void kv8_consumers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// tm_k, tm_v: the caches as {D, n_pages * Hkv * P} bytes, box {D, P}.  NRT: groups of eight query heads (a
-// power of two).
-template <int D, int NRT>
-__global__ void __launch_bounds__(Kv8Cfg<D>::THREADS, 1) kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
-                                                                        const __grid_constant__ CUtensorMap tm_v,
-                                                                        const Kv8AttnParams p) {
-    using C = Kv8Cfg<D>;
-    constexpr int KS = C::CONSUMERS / NRT;        // warps that share the keys of a group of heads
+// tm_k, tm_v: the caches as {D, n_pages * Hkv * P} bytes, box {D, min(P, 64)}.
+template <int D, int NT, int NRG>
+__global__ void __launch_bounds__(Kv8Cfg<D, NT, NRG>::THREADS, Kv8Cfg<D, NT, NRG>::BLOCKS_PER_SM)
+    kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const Kv8AttnParams p) {
+    using C = Kv8Cfg<D, NT, NRG>;
     constexpr int NSTEP = D / 16;                 // mma steps along the features
     constexpr int VW = D / 32;                    // 32-bit words of a lane's features of one value row
     extern __shared__ __align__(1024) uint8_t dsmem[];
     uint8_t* smem = dsmem + ((1024u - (smem_u32(dsmem) & 1023u)) & 1023u);
     float* s_o = reinterpret_cast<float*>(smem + C::OFF_O);
     float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
-    float* s_l = s_m + C::CONSUMERS * 8;
+    float* s_l = s_m + C::CONSUMERS * C::HEADS;
+    uint2* s_q = reinterpret_cast<uint2*>(smem + C::OFF_Q);
     float4* s_meta = reinterpret_cast<float4*>(smem + C::OFF_META);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* empty = full + C::NS;
-    __shared__ long long s_warp_sum[C::CONSUMERS + 1];
-    __shared__ long long s_before;
-    __shared__ int s_first, s_last;
+    __shared__ int s_warp_sum[C::CONSUMERS + 1];
+    __shared__ int s_before, s_first, s_last;
 
     const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31u);
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(smem_u32(full + s), 1);
-            mbar_init(smem_u32(empty + s), C::CONSUMERS);
+            mbar_init(smem_u32(empty + s), C::CONSUMERS / C::SETS);
         }
         fence_barrier_init();
         tma_prefetch_desc(&tm_k);
@@ -319,31 +460,31 @@ __global__ void __launch_bounds__(Kv8Cfg<D>::THREADS, 1) kv8_attn_kernel(const _
     Kv8Walk w;
     const int per = (p.B + C::THREADS - 1) / C::THREADS;
     const int b_lo = min(p.B, (int)threadIdx.x * per), b_hi = min(p.B, b_lo + per);
-    long long mine = 0;
+    int mine = 0;
     for (w.b = b_lo; w.b < b_hi; ++w.b) {
         w.load(p);
         mine += w.nch;
     }
-    long long incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += o;
     }
     if (lane == 31) s_warp_sum[warp] = incl;
     __syncthreads();
-    long long total = 0;
+    int total = 0;
 #pragma unroll
     for (int i = 0; i <= C::CONSUMERS; ++i) {
         if (i == warp) incl += total;
         total += s_warp_sum[i];
     }
-    const long long n_units = total * p.c.Hkv;
-    const int n_blocks = (int)min((long long)gridDim.x, n_units);
+    const int n_units = total * p.c.Hkv;
+    const int n_blocks = min((int)gridDim.x, n_units);
     if ((int)blockIdx.x >= n_blocks) return;
-    const long long u0 = n_units * blockIdx.x / n_blocks, u1 = n_units * (blockIdx.x + 1) / n_blocks;
+    const int u0 = kv8_first_unit(blockIdx.x, n_units, n_blocks), u1 = kv8_first_unit(blockIdx.x + 1, n_units, n_blocks);
     if (u0 >= (incl - mine) * p.c.Hkv && u0 < incl * p.c.Hkv) {
-        long long before = incl - mine;
+        int before = incl - mine;
         for (w.b = b_lo;; ++w.b) {
             w.load(p);
             if (u0 < (before + w.nch) * p.c.Hkv) break;
@@ -355,36 +496,35 @@ __global__ void __launch_bounds__(Kv8Cfg<D>::THREADS, 1) kv8_attn_kernel(const _
     __syncthreads();
     w.b = s_first;
     w.load(p);
-    {
-        const long long r = u0 - s_before * p.c.Hkv;
-        w.hk = (int)(r / w.nch);
-        w.begin = s_before * p.c.Hkv + (long long)w.hk * w.nch;
-    }
+    w.hk = (u0 - s_before * p.c.Hkv) / w.nch;
+    w.begin = s_before * p.c.Hkv + w.hk * w.nch;
 
     if (warp == C::CONSUMERS) {
         // ------------------------------------------------------------------------------- producer
-        const int np_log = 7 - p.c.log_p;                  // pages of a chunk
-        const int P = 1 << p.c.log_p, tiles = P / 16;
-        const uint32_t page_bytes = (uint32_t)(P * D);
+        // A box is a page, or the half of a 128-token page that a chunk has.
+        const int box_log = min(p.c.log_p, 6), nb_log = 6 - box_log;   // 64 >> nb_log keys; boxes of a chunk
+        const int tiles = (1 << box_log) / 16;
+        const uint32_t box_bytes = (uint32_t)((1 << box_log) * D);
         bool waited = false, ok = true;
         int i = 0;
-        for (long long u = u0; u < u1 && ok; w.next(p)) {
-            const long long end = min(u1, w.begin + w.nch);
-            const int c_end = w.ch0 + (int)(end - w.begin);
-            int c = w.ch0 + (int)(u - w.begin);
+        for (int u = u0; u < u1 && ok; w.next(p)) {
+            const int end = min(u1, w.begin + w.nch);
+            const int c_end = w.ch0 + (end - w.begin);
+            int c = w.ch0 + (u - w.begin);
             u = end;
-            int base = 0, page = -1;                       // chunk of lane 0's page; this lane's page
+            int base = 0, row = -1;                        // chunk of lane 0's box; this lane's box: its row in the cache
             float ks = 0.f, vs = 0.f;
             for (int left = 0; c < c_end; ++c, --left) {
                 if (left == 0) {
-                    // the pages of the next 32 >> np_log chunks
-                    left = 32 >> np_log;
+                    // the boxes of the next 32 >> nb_log chunks
+                    left = 32 >> nb_log;
                     base = c;
-                    const int j = (c << np_log) + lane;
+                    const long long pos = (long long)c * kKv8Chunk + ((long long)lane << box_log);
                     const int c_stop = min(c_end, c + left);
-                    page = -1;
-                    if ((long long)j * P < min((long long)w.n, (long long)c_stop * kKv8Chunk) && (j + 1) * (long long)P > w.lo) {
-                        page = __ldg(p.table + (long long)w.b * p.max_pages + j);
+                    row = -1;
+                    int page = -1;
+                    if (pos < min((long long)w.n, (long long)c_stop * kKv8Chunk) && pos + (1 << box_log) > w.lo) {
+                        page = __ldg(p.table + (long long)w.b * p.max_pages + (int)(pos >> p.c.log_p));
                         if (page < 0 || page >= p.c.n_pages) {
                             record_error(kErrIndex, kSiteKvPage);
                             page = -1;
@@ -397,8 +537,10 @@ __global__ void __launch_bounds__(Kv8Cfg<D>::THREADS, 1) kv8_attn_kernel(const _
                         waited = true;
                     }
                     if (page >= 0) {
-                        ks = p.c.k_scale[(long long)page * p.c.Hkv + w.hk];
-                        vs = p.c.v_scale[(long long)page * p.c.Hkv + w.hk];
+                        const int ph = page * p.c.Hkv + w.hk;
+                        ks = p.c.k_scale[ph];
+                        vs = p.c.v_scale[ph];
+                        row = (ph << p.c.log_p) + ((int)pos & ((1 << p.c.log_p) - 1));
                     }
                 }
                 const int s = i % C::NS;
@@ -407,22 +549,21 @@ __global__ void __launch_bounds__(Kv8Cfg<D>::THREADS, 1) kv8_attn_kernel(const _
                     ok = false;
                     break;
                 }
-                const int rel = lane - ((c - base) << np_log);         // this lane's page within the chunk
-                const bool here = rel >= 0 && rel < (1 << np_log);
-                const bool load = here && page >= 0;
+                const int rel = lane - ((c - base) << nb_log);         // this lane's box within the chunk
+                const bool here = rel >= 0 && rel < (1 << nb_log);
+                const bool load = here && row >= 0;
                 if (here)
                     for (int k = 0; k < tiles; ++k)
-                        s_meta[s * 8 + rel * tiles + k] =
-                            make_float4(ks * p.c1, page >= 0 ? vs : -1.f, log2f(vs), 0.f);
+                        s_meta[s * kKv8Tiles + rel * tiles + k] =
+                            make_float4(ks * p.c1, row >= 0 ? vs : -1.f, log2f(vs), 0.f);
                 const uint32_t n_load = (uint32_t)__popc(__ballot_sync(0xffffffffu, load));
                 const uint32_t bar = smem_u32(full + s);
-                if (lane == 0) mbar_arrive_expect_tx(bar, n_load * 2u * page_bytes);
+                if (lane == 0) mbar_arrive_expect_tx(bar, n_load * 2u * box_bytes);
                 __syncwarp();
                 if (load) {
-                    const uint32_t dst = smem_u32(smem) + (uint32_t)(2 * s) * C::TENSOR + (uint32_t)rel * page_bytes;
-                    const int y = (page * p.c.Hkv + w.hk) << p.c.log_p;
-                    tma_load_2d(dst, &tm_k, bar, 0, y);
-                    tma_load_2d(dst + C::TENSOR, &tm_v, bar, 0, y);
+                    const uint32_t dst = smem_u32(smem) + (uint32_t)(2 * s) * C::TENSOR + (uint32_t)rel * box_bytes;
+                    tma_load_2d(dst, &tm_k, bar, 0, row);
+                    tma_load_2d(dst + C::TENSOR, &tm_v, bar, 0, row);
                 }
                 ++i;
             }
@@ -436,143 +577,55 @@ __global__ void __launch_bounds__(Kv8Cfg<D>::THREADS, 1) kv8_attn_kernel(const _
 
     // ----------------------------------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3;
-    const int rt = warp % NRT, sub = warp / NRT;
+    const int rg = warp % NRG, kslot = warp / NRG;             // set of heads, share of the keys
+    const int set = kslot / kKv8Tiles % C::SETS;
+    const int h_base = rg * C::HEADS;                          // this warp's first head in the group
+    const uint4* q_lane = reinterpret_cast<const uint4*>(s_q) + rg * NT * (NSTEP / 2) * 32 + lane;
     grid_dependency_wait();
     bool ok = true;
     int i = 0;
-    for (long long u = u0; u < u1;) {
-        const long long end = min(u1, w.begin + w.nch);
-        const int c_begin = w.ch0 + (int)(u - w.begin), c_end = w.ch0 + (int)(end - w.begin);
-        // qhat of heads rt * 8 + g: features in the order of the key rows' bytes
-        uint32_t q[NSTEP][2];
-        {
-            const int hg = rt * 8 + g;
-            const __nv_bfloat16* qr = p.qh + ((long long)w.b * p.H + (long long)w.hk * p.G + hg) * D;
-#pragma unroll
-            for (int st = 0; st < NSTEP; ++st) {
-                const int f = D == 128 ? 32 * t + 4 * st : 16 * t + 4 * st;
-                uint2 raw = make_uint2(0u, 0u);
-                if (hg < p.G) raw = *reinterpret_cast<const uint2*>(qr + f);
-                q[st][0] = pack_half2(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u));
-                q[st][1] = pack_half2(__uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u));
-            }
+    for (int u = u0; u < u1;) {
+        const int end = min(u1, w.begin + w.nch);
+        const int c_begin = w.ch0 + (u - w.begin), c_end = w.ch0 + (end - w.begin);
+        // qhat of the group's heads as the products' B operands: groups of eight heads, steps, lanes
+        for (int x = (int)threadIdx.x; x < C::NTG * NSTEP * 32; x += 256) {
+            const int xl = x & 31, st = (x >> 5) % NSTEP, hg = 8 * (x / (32 * NSTEP)) + (xl >> 2);
+            const int f = (D == 128 ? 32 : 16) * (xl & 3) + 4 * st;    // features in the order of a key row's bytes
+            uint2 raw = make_uint2(0u, 0u);
+            if (hg < p.G)
+                raw = *reinterpret_cast<const uint2*>(p.qh + ((long long)w.b * p.H + (long long)w.hk * p.G + hg) * D + f);
+            s_q[((x >> 5) / 2 * 32 + xl) * 2 + (st & 1)] =
+                make_uint2(pack_half2(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u)),
+                           pack_half2(__uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)));
         }
-        float o[2 * VW][4];
+        kv8_consumers_sync();              // and the last piece's results have been read
+        float o[NT][2 * VW][4];
+        float m[NT][2], l[NT][2];                              // heads 2 t and 2 t + 1 of each group
 #pragma unroll
-        for (int k = 0; k < 2 * VW; ++k)
+        for (int x = 0; x < NT; ++x) {
+            m[x][0] = m[x][1] = -INFINITY;
+            l[x][0] = l[x][1] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;      // heads 2 t and 2 t + 1
+            for (int k = 0; k < 2 * VW; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x][k][e] = 0.f;
+        }
 
         for (int c = c_begin; c < c_end; ++c, ++i) {
+            if (C::SETS > 1 && i % C::SETS != set) continue;
             const int s = i % C::NS;
             if (ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(full + s), (uint32_t)(i / C::NS) & 1u, p.wait_limit_ns,
                                                          kSiteKv8Full)))
                 ok = false;
             if (!ok) break;
-            const uint8_t* kt = smem + (2 * s) * C::TENSOR;
-#pragma unroll 1
-            for (int tile = sub; tile < 8; tile += KS) {
+            {
+                const int tile = kslot % kKv8Tiles;
                 const int pos0 = c * kKv8Chunk + 16 * tile;
-                if (pos0 + 16 <= w.lo || pos0 >= w.n) continue;
-                const float4 meta = s_meta[s * 8 + tile];
-                if (meta.y < 0.f) continue;                            // a page that is not there
-                const bool whole = pos0 >= w.lo && pos0 + 16 <= w.n;
-                const uint8_t* kr = kt + tile * 16 * D;
-                const uint8_t* vr = kr + C::TENSOR;
-                uint32_t a[2][VW * 2];                                 // rows g, g + 8
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int x = 0; x < D / 64; ++x) {
-                        const int row = g + 8 * r;
-                        const int at = D == 128 ? row * 128 + (((2 * t + x) ^ (row & 7)) << 4)
-                                                : row * 64 + ((t ^ ((row >> 1) & 3)) << 4);
-                        const uint4 v4 = *reinterpret_cast<const uint4*>(kr + at);
-                        a[r][4 * x] = v4.x;
-                        a[r][4 * x + 1] = v4.y;
-                        a[r][4 * x + 2] = v4.z;
-                        a[r][4 * x + 3] = v4.w;
-                    }
-                uint32_t v[4][VW];                                     // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int row = 2 * t + (x & 1) + 8 * (x >> 1);
-                    if (D == 128) {
-                        const uint4 v4 = *reinterpret_cast<const uint4*>(vr + row * 128 + ((g ^ (row & 7)) << 4));
-                        v[x][0] = v4.x;
-                        v[x][1] = v4.y;
-                        v[x][VW - 2] = v4.z;
-                        v[x][VW - 1] = v4.w;
-                    } else {
-                        const uint2 v2 = *reinterpret_cast<const uint2*>(vr + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) +
-                                                                         8 * (g & 1));
-                        v[x][0] = v2.x;
-                        v[x][1] = v2.y;
-                    }
-                }
-                // S^T, two chains
-                float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int st = 0; st < NSTEP; ++st) {
-                    const uint32_t a0 = fp8x2_to_half2(a[0][st]), a1 = fp8x2_to_half2(a[1][st]);
-                    const uint32_t a2 = fp8x2_to_half2(a[0][st] >> 16), a3 = fp8x2_to_half2(a[1][st] >> 16);
-                    mma_16816((st & 1) ? s1 : s0, a0, a1, a2, a3, q[st][0], q[st][1]);
-                }
-                float x0 = (s0[0] + s1[0]) * meta.x, x1 = (s0[1] + s1[1]) * meta.x;    // key g
-                float x2 = (s0[2] + s1[2]) * meta.x, x3 = (s0[3] + s1[3]) * meta.x;    // key g + 8
-                if (!whole) {
-                    // keys outside [lo, n): weight 0 whatever the page holds there
-                    if (pos0 + g < w.lo || pos0 + g >= w.n) x0 = x1 = -INFINITY;
-                    if (pos0 + g + 8 < w.lo || pos0 + g + 8 >= w.n) x2 = x3 = -INFINITY;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int key = pos0 + 2 * t + (x & 1) + 8 * (x >> 1);
-                        if (key < w.lo || key >= w.n)
-#pragma unroll
-                            for (int k = 0; k < VW; ++k) v[x][k] = 0u;
-                    }
-                }
-                float t0 = fmaxf(x0, x2) + meta.z, t1 = fmaxf(x1, x3) + meta.z;
-                if (__any_sync(0xffffffffu, t0 > m0 + kSlack || t1 > m1 + kSlack)) {
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) {
-                        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
-                        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
-                    }
-                    t0 = fmaxf(t0, m0);
-                    t1 = fmaxf(t1, m1);
-                    const float f0 = ex2_approx(m0 - t0), f1 = ex2_approx(m1 - t1);
-                    m0 = t0;
-                    m1 = t1;
-                    l0 *= f0;
-                    l1 *= f1;
-#pragma unroll
-                    for (int k = 0; k < 2 * VW; ++k) {
-                        o[k][0] *= f0;
-                        o[k][1] *= f1;
-                        o[k][2] *= f0;
-                        o[k][3] *= f1;
-                    }
-                }
-                x0 = ex2_approx(x0 - m0);
-                x1 = ex2_approx(x1 - m1);
-                x2 = ex2_approx(x2 - m0);
-                x3 = ex2_approx(x3 - m1);
-                l0 += x0 + x2;
-                l1 += x1 + x3;
-                const uint32_t b0 = movmatrix_trans(pack_half2(x0 * meta.y, x1 * meta.y));
-                const uint32_t b1 = movmatrix_trans(pack_half2(x2 * meta.y, x3 * meta.y));
-#pragma unroll
-                for (int k = 0; k < VW; ++k) {
-                    // features 4 k .. 4 k + 3 of this lane, keys (2 t, 2 t + 1) and (2 t + 8, 2 t + 9)
-                    const uint32_t p0 = __byte_perm(v[0][k], v[1][k], 0x5140), p1 = __byte_perm(v[2][k], v[3][k], 0x5140);
-                    const uint32_t r0 = __byte_perm(v[0][k], v[1][k], 0x7362), r1 = __byte_perm(v[2][k], v[3][k], 0x7362);
-                    mma_16816(o[2 * k], fp8x2_to_half2(p0), fp8x2_to_half2(p0 >> 16), fp8x2_to_half2(p1),
-                              fp8x2_to_half2(p1 >> 16), b0, b1);
-                    mma_16816(o[2 * k + 1], fp8x2_to_half2(r0), fp8x2_to_half2(r0 >> 16), fp8x2_to_half2(r1),
-                              fp8x2_to_half2(r1 >> 16), b0, b1);
-                }
+                const float4 meta = s_meta[s * kKv8Tiles + tile];
+                // not wanted: outside the visible keys, or on a page that is not there
+                if (pos0 + 16 > w.lo && pos0 < w.n && meta.y >= 0.f)
+                    kv8_tile<D, NT>(smem + (2 * s) * C::TENSOR + tile * 16 * D, C::TENSOR, pos0, w.lo, w.n, meta, q_lane, o, m, l,
+                                    g, t);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(empty + s));
@@ -580,38 +633,70 @@ __global__ void __launch_bounds__(Kv8Cfg<D>::THREADS, 1) kv8_attn_kernel(const _
 
         // The piece's result: the warps' sums joined.
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-        }
-        kv8_consumers_sync();              // the last piece's results have been read
-        if (g == 0) {
-            s_m[warp * 8 + 2 * t] = m0;
-            s_m[warp * 8 + 2 * t + 1] = m1;
-            s_l[warp * 8 + 2 * t] = l0;
-            s_l[warp * 8 + 2 * t + 1] = l1;
-        }
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (rt * 8 + 2 * t + e < p.G)
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int k = 0; k < 2 * VW; ++k)
-                    *reinterpret_cast<float2*>(s_o + (warp * 8 + 2 * t + e) * D + 4 * VW * g + 2 * k) =
-                        make_float2(o[k][e], o[k][2 + e]);
+                for (int d = 4; d < 32; d <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], d);
+        // warp `at` of the buffer; heads past the group are left out
+        auto put = [&](int at) {
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int hc = 8 * x + 2 * t + e;
+                    if (h_base + hc >= p.G) continue;
+                    if (g == 0) {
+                        s_m[at * C::HEADS + hc] = m[x][e];
+                        s_l[at * C::HEADS + hc] = l[x][e];
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2 * VW; ++k)
+                        *reinterpret_cast<float2*>(s_o + (at * C::HEADS + hc) * D + 4 * VW * g + 2 * k) =
+                            make_float2(o[x][k][e], o[x][k][2 + e]);
+                }
+        };
+        const bool upper = warp >= C::CONSUMERS / 2;
+        if (upper) put(warp - C::CONSUMERS / 2);
+        kv8_consumers_sync();
+        if (!upper) {
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int hc = 8 * x + 2 * t + e;
+                    if (h_base + hc >= p.G) continue;
+                    const int at = warp * C::HEADS + hc;
+                    const float m2 = s_m[at], l2 = s_l[at];
+                    const float M = fmaxf(m[x][e], m2);
+                    const float f1 = kv8_factor(m[x][e], l[x][e], M), f2 = kv8_factor(m2, l2, M);
+#pragma unroll
+                    for (int k = 0; k < 2 * VW; ++k) {
+                        const float2 o2 = *reinterpret_cast<const float2*>(s_o + at * D + 4 * VW * g + 2 * k);
+                        o[x][k][e] = o[x][k][e] * f1 + o2.x * f2;
+                        o[x][k][2 + e] = o[x][k][2 + e] * f1 + o2.y * f2;
+                    }
+                    m[x][e] = M;
+                    l[x][e] = l[x][e] * f1 + l2 * f2;
+                }
+        }
+        __syncwarp();
+        if (!upper) put(warp);             // where it has just read
         kv8_consumers_sync();
         const bool alone = u == w.begin && end == w.begin + w.nch;
         const int slot = 2 * (int)blockIdx.x + (u0 < w.begin ? 1 : 0);
         for (int x = (int)threadIdx.x; x < p.G * D; x += 256) {
             const int h = x / D, d = x % D;
-            const int hr = h >> 3, hc = h & 7;
+            const int r = h / C::HEADS, hc = h % C::HEADS;
+            constexpr int KH = C::KSLOTS / 2;
             float M = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) M = fmaxf(M, s_m[(k * NRT + hr) * 8 + hc]);
+            for (int k = 0; k < KH; ++k) M = fmaxf(M, s_m[(k * NRG + r) * C::HEADS + hc]);
             float L = 0.f, O = 0.f;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const int at = (k * NRT + hr) * 8 + hc;
-                const float f = s_m[at] == -INFINITY && s_l[at] == 0.f ? 0.f : ex2_approx(s_m[at] - M);
+            for (int k = 0; k < KH; ++k) {
+                const int at = (k * NRG + r) * C::HEADS + hc;
+                const float f = kv8_factor(s_m[at], s_l[at], M);
                 L = fmaf(s_l[at], f, L);
                 O = fmaf(s_o[at * D + d], f, O);
             }
@@ -638,7 +723,7 @@ __global__ void __launch_bounds__(Kv8Cfg<D>::THREADS, 1) kv8_attn_kernel(const _
             kv8_consumers_sync();
             if (s_last) {
                 __threadfence();
-                const int first_slot = 2 * c_first + (n_units * c_first / n_blocks < w.begin ? 1 : 0);
+                const int first_slot = 2 * c_first + (kv8_first_unit(c_first, n_units, n_blocks) < w.begin ? 1 : 0);
                 for (int x = (int)threadIdx.x; x < p.G * D; x += 256) {
                     const int h = x / D, d = x % D;
                     auto at = [&](int k) {
@@ -648,7 +733,7 @@ __global__ void __launch_bounds__(Kv8Cfg<D>::THREADS, 1) kv8_attn_kernel(const _
                     for (int k = 0; k < pieces; ++k) M = fmaxf(M, __ldcg(at(k) + D));
                     for (int k = 0; k < pieces; ++k) {
                         const float mk = __ldcg(at(k) + D), lk = __ldcg(at(k) + D + 1);
-                        const float f = mk == -INFINITY && lk == 0.f ? 0.f : ex2_approx(mk - M);
+                        const float f = kv8_factor(mk, lk, M);
                         L = fmaf(lk, f, L);
                         O = fmaf(__ldcg(at(k) + d), f, O);
                     }

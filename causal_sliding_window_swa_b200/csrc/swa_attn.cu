@@ -1398,8 +1398,9 @@ struct Kv8DecLayout {
 Kv8DecLayout kv8_dec_layout(const Shape& s) {
     Kv8DecLayout w{};
     w.counters = round_up((size_t)s.n * 2);
-    w.part = w.counters + round_up(swa::kKv8MaxBlocks * sizeof(int));
-    w.total = w.part + round_up((size_t)2 * swa::kKv8MaxBlocks * (s.H / s.Hkv) * (s.D + 4) * sizeof(float));
+    const int G = s.H / s.Hkv;
+    w.part = w.counters + round_up(swa::kv8_max_blocks(G) * sizeof(int));
+    w.total = w.part + round_up((size_t)2 * swa::kv8_max_blocks(G) * G * (s.D + 4) * sizeof(float));
     return w;
 }
 
@@ -1410,49 +1411,48 @@ int check_kv8_heads(int B, int H, int Hkv, int D, Shape* s) {
     return rc;
 }
 
-// The pages as {D, n_pages * Hkv * P} bytes; box = one page of one head.
-bool make_page_map(CUtensorMap* m, const void* base, long long rows, int D, int P) {
+// The pages as {D, n_pages * Hkv * P} bytes; box = box_rows tokens of one page and head.
+bool make_page_map(CUtensorMap* m, const void* base, long long rows, int D, int box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)D};
-    const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)P};
+    const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NRT>
-bool set_kv8_smem() {
-    return cudaFuncSetAttribute(swa::kv8_attn_kernel<D, NRT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                swa::Kv8Cfg<D>::SMEM) == cudaSuccess;
+template <int D, int NT, int NRG>
+int launch_kv8_attention_n(int dev, const CUtensorMap& tk, const CUtensorMap& tv, const swa::Kv8AttnParams& a,
+                           cudaStream_t st) {
+    using C = swa::Kv8Cfg<D, NT, NRG>;
+    static std::once_flag once[64];
+    static bool ok[64] = {false};
+    std::call_once(once[dev], [&] {
+        ok[dev] = cudaFuncSetAttribute(swa::kv8_attn_kernel<D, NT, NRG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::SMEM) == cudaSuccess;
+    });
+    if (!ok[dev]) {
+        cudaGetLastError();
+        return SWA_ERR_CUDA;
+    }
+    const int blocks = std::min(g_num_sms[dev], swa::kKv8Sms) * C::BLOCKS_PER_SM;
+    launch_pdl(swa::kv8_attn_kernel<D, NT, NRG>, dim3((unsigned)blocks), dim3(C::THREADS), C::SMEM, st, tk, tv, a);
+    return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
 template <int D>
 int launch_kv8_attention(int dev, const swa::Kv8AttnParams& a, cudaStream_t st) {
-    using C = swa::Kv8Cfg<D>;
-    {
-        static std::once_flag once[64];
-        static bool ok[64] = {false};
-        std::call_once(once[dev], [&] {
-            ok[dev] = set_kv8_smem<D, 1>() && set_kv8_smem<D, 2>() && set_kv8_smem<D, 4>() && set_kv8_smem<D, 8>();
-        });
-        if (!ok[dev]) {
-            cudaGetLastError();
-            return SWA_ERR_CUDA;
-        }
-    }
     CUtensorMap tk, tv;
     const long long rows = ((long long)a.c.n_pages * a.c.Hkv) << a.c.log_p;
-    if (!make_page_map(&tk, a.c.k_cache, rows, D, 1 << a.c.log_p) || !make_page_map(&tv, a.c.v_cache, rows, D, 1 << a.c.log_p))
-        return SWA_ERR_CUDA;
-    const dim3 grid((unsigned)std::min(g_num_sms[dev], swa::kKv8MaxBlocks)), block(C::THREADS);
-    if (a.G <= 8) launch_pdl(swa::kv8_attn_kernel<D, 1>, grid, block, C::SMEM, st, tk, tv, a);
-    else if (a.G <= 16) launch_pdl(swa::kv8_attn_kernel<D, 2>, grid, block, C::SMEM, st, tk, tv, a);
-    else if (a.G <= 32) launch_pdl(swa::kv8_attn_kernel<D, 4>, grid, block, C::SMEM, st, tk, tv, a);
-    else launch_pdl(swa::kv8_attn_kernel<D, 8>, grid, block, C::SMEM, st, tk, tv, a);
-    return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+    const int box = std::min(1 << a.c.log_p, swa::kKv8Chunk);
+    if (!make_page_map(&tk, a.c.k_cache, rows, D, box) || !make_page_map(&tv, a.c.v_cache, rows, D, box)) return SWA_ERR_CUDA;
+    if (a.G <= 8) return launch_kv8_attention_n<D, 1, 1>(dev, tk, tv, a, st);
+    if (a.G <= 16) return launch_kv8_attention_n<D, 2, 1>(dev, tk, tv, a, st);
+    if (a.G <= 32) return launch_kv8_attention_n<D, 4, 1>(dev, tk, tv, a, st);
+    return launch_kv8_attention_n<D, 4, 2>(dev, tk, tv, a, st);
 }
 
 }  // namespace
@@ -1481,7 +1481,10 @@ int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void*
     if (rc == SWA_OK) rc = check_cache(k_cache, v_cache, k_scale, v_scale);
     if (rc != SWA_OK) return rc;
     if (!block_table || !seq_len || !workspace || max_pages < 1) return SWA_ERR_INVALID_ARG;
-    if ((long long)max_pages * page_size >= (1ll << 31)) return SWA_ERR_UNSUPPORTED;
+    // positions and the attention's units (64 positions of a request and head) within int32
+    if ((long long)max_pages * page_size >= (1ll << 31) ||
+        ((long long)max_pages * page_size / swa::kKv8Chunk + 1) * B * Hkv >= (1ll << 31))
+        return SWA_ERR_UNSUPPORTED;
     if (!aligned(block_table, 4) || !aligned(seq_len, 4) || (doc_start && !aligned(doc_start, 4)) || !aligned(workspace, 16))
         return SWA_ERR_MISALIGNED;
     const Kv8DecLayout L = kv8_dec_layout(s);
@@ -1497,7 +1500,7 @@ int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void*
     const swa::Kv8TokenParams t{static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v),
                                 static_cast<const bf*>(ve), static_cast<const bf*>(gate_x), static_cast<const bf*>(Wg),
                                 block_table, seq_len, reinterpret_cast<bf*>(ws + L.qh), static_cast<bf*>(out), lse, c, H,
-                                max_pages, counters, swa::kKv8MaxBlocks, (double)rope_base, (double)eps};
+                                max_pages, counters, swa::kv8_max_blocks(H / Hkv), (double)rope_base, (double)eps};
     const int rows = 256 / (D / 8);
     const dim3 tg((unsigned)B, (unsigned)((H + (k ? Hkv : 0) + rows - 1) / rows));
     const swa::Kv8AttnParams a{reinterpret_cast<const bf*>(ws + L.qh), block_table, seq_len, doc_start, static_cast<bf*>(out),

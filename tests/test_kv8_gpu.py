@@ -316,6 +316,54 @@ def test_decode_matches_the_plain_statement(case):
     swa.check_device_status()
 
 
+@pytest.mark.parametrize("B,H,Hkv,D,P,window,most", [
+    (24, 8, 8, 128, 64, 0, 3000), (40, 8, 8, 64, 16, 0, 2500), (60, 16, 2, 128, 32, 2000, 4000), (30, 12, 6, 64, 128, 0, 5000),
+    (50, 30, 2, 128, 64, 0, 6000), (90, 24, 1, 64, 16, 5000, 9000), (60, 32, 1, 128, 128, 0, 9000), (60, 48, 1, 128, 64, 0, 5000),
+    (100, 64, 1, 64, 32, 0, 4000), (256, 12, 12, 128, 64, 0, 129), (1000, 3, 3, 64, 16, 100, 200),
+])
+def test_decode_many_units_for_each_block(B, H, Hkv, D, P, window, most):
+    """Many chunks of keys for each block, so that the ring of stages goes round many times: all requests against 64-bit
+    attention over what kv8_read returns of the cache (which the tests above hold to the plain codes)."""
+    g = torch.Generator("cuda").manual_seed(B + D)
+    r = random.Random(B)
+    lens = [most] + [r.choice([0, 1, 64, 65, r.randint(1, most), r.randint(most // 2, most)]) for _ in range(B - 1)]
+    cnt = [-(-n // P) for n in lens]
+    n_pages = sum(cnt) + 1
+    perm = torch.randperm(n_pages, generator=g, device="cuda").int()
+    table = torch.full((B, max(cnt)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, c in enumerate(cnt):
+        table[b, :c] = perm[at:at + c]
+        at += c
+    cache = []
+    for _ in "kv":
+        x = torch.randn((n_pages, Hkv, P, D), generator=g, device="cuda") * 64
+        cache.append(x.to(torch.float8_e4m3fn))
+    ks = torch.full((n_pages, Hkv), 2.0 ** -6, device="cuda")
+    vs = torch.exp2(torch.randint(-9, 3, (n_pages, Hkv), generator=g, device="cuda").float())
+    q = torch.randn((B, H, D), generator=g, device="cuda").to(torch.bfloat16)
+    for _ in range(3):
+        out, lse = swa.decode_kv8(q, None, None, *cache, ks, vs, table, i32(lens), window)
+    swa.check_device_status()
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert (out[b] == 0).all() and (lse[b] == float("-inf")).all()
+            continue
+        lo = kv8_plain.visible(n, window, 0)
+        pos = torch.arange(lo, n, device="cuda")
+        slots = (table[b, pos // P].long() * P + pos % P).int()[None].contiguous()
+        k, v = (t[0].double().transpose(0, 1) for t in swa.kv8_read(slots, *cache, ks, vs))      # (Hkv, n, D)
+        qh = bf16(kv8_plain.prologue(f64(q[b]), n - 1)).double().cuda().view(Hkv, H // Hkv, D)
+        s = qh @ k.transpose(1, 2) / D ** 0.5
+        p = torch.softmax(s, -1)
+        ref, mag = (p @ v).reshape(H, D).cpu().numpy(), (p @ v.abs()).reshape(H, D).cpu().numpy()
+        ref_l = torch.logsumexp(s, -1).reshape(H).cpu().numpy()
+        worst = np.abs(f64(out[b]) - ref) / kv8_plain.out_tolerance(ref, mag)
+        assert worst.max() <= 1, (b, n, worst.max())
+        # the keys here are rows of root mean square up to 1.3
+        assert (np.abs(f64(lse[b]) - ref_l) <= 2 * kv8_plain.lse_tolerance(ref_l, D)).all(), (b, n)
+
+
 def test_adversarial_scores_and_scales():
     # keys along the query and against it, so that probabilities span the whole range; values of very different size in
     # neighbouring pages
