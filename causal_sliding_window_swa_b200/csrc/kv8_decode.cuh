@@ -8,6 +8,9 @@
 // Requests with n_b <= 0 are empty rows: out = 0, lse = -inf.
 #pragma once
 
+#include <climits>
+
+#include "decode.cuh"
 #include "kv8.cuh"
 
 namespace swa {
@@ -40,122 +43,154 @@ __device__ __forceinline__ int kv8_length(const int* seq_len, int b, int max_pag
     return n <= 0 || (long long)n > ((long long)max_pages << log_p) ? 0 : n;
 }
 
+// Entry i of the RoPE row of `pos`, in the split of the prefill table.
+template <int D>
+__device__ __forceinline__ void kv8_rope_entry(double base, int pos, int i, float4* s_tab32, double2* s_tab64) {
+    const double theta = pow(base, -2.0 * (double)i / (double)D);
+    double sn, cs;
+    sincos((double)pos * theta, &sn, &cs);
+    float c_hi, c_lo, s_hi, s_lo;
+    rope_split(cs, c_hi, c_lo);
+    rope_split(sn, s_hi, s_lo);
+    s_tab32[i] = make_float4(c_hi, c_lo, s_hi, s_lo);
+    s_tab64[i] = make_double2(cs, sn);
+}
+
+// The empty row of heads [h0, h0 + heads) of request b, by all threads of the block.
+template <int D>
+__device__ __forceinline__ void kv8_empty_row(__nv_bfloat16* out, float* lse, long long row0, int heads) {
+    for (int i = threadIdx.x; i < heads * (D / 8); i += blockDim.x)
+        reinterpret_cast<uint4*>(out + row0 * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (lse != nullptr)
+        for (int i = threadIdx.x; i < heads; i += blockDim.x) lse[row0 + i] = -INFINITY;
+}
+
+// One row of request b's new token, D/8 lanes (this one is lane c): query head `h` (kQuery), or key/value head `h`
+// (kKeyValue), whose khat and v' go into the cache.  load() issues the loads; finish(), once the RoPE row is
+// there, is called by whole warps.
+enum { kNoRow = 0, kQuery = 1, kKeyValue = 2 };
+template <int D>
+struct Kv8Row {
+    int kind, h, page;
+    uint2 x0, x1, v0, v1, e0, e1;
+    float2 gw;
+    float old_scale[2];
+
+    __device__ __forceinline__ void load(const Kv8TokenParams& p, int b, int pos, int kind_, int h_, int c) {
+        constexpr int HALF = D / 2;
+        const int i0 = 4 * c, Hkv = p.c.Hkv;
+        kind = kind_;
+        h = h_;
+        page = -1;
+        x0 = x1 = v0 = v1 = e0 = e1 = make_uint2(0u, 0u);
+        gw = make_float2(0.f, 0.f);
+        old_scale[0] = old_scale[1] = 1.f;
+        if (kind != kNoRow) {
+            const __nv_bfloat16* src =
+                kind == kQuery ? p.q + ((long long)b * p.H + h) * D : p.k + ((long long)b * Hkv + h) * D;
+            x0 = ldg_stream8(src + i0);
+            x1 = ldg_stream8(src + HALF + i0);
+        }
+        if (kind == kKeyValue) {
+            const __nv_bfloat16* vr = p.v + ((long long)b * Hkv + h) * D;
+            v0 = ldg_stream8(vr + i0);
+            v1 = ldg_stream8(vr + HALF + i0);
+            page = __ldg(p.table + (long long)b * p.max_pages + (pos >> p.c.log_p));
+            if (page < 0 || page >= p.c.n_pages) {
+                if (c == 0) record_error(kErrIndex, kSiteKvPage);
+                page = -1;
+            } else {
+                old_scale[0] = p.c.k_scale[(long long)page * Hkv + h];
+                old_scale[1] = p.c.v_scale[(long long)page * Hkv + h];
+            }
+            if (p.ve != nullptr) {
+                const __nv_bfloat16* er = p.ve + ((long long)b * Hkv + h) * D;
+                e0 = ldg_stream8(er + i0);
+                e1 = ldg_stream8(er + HALF + i0);
+                // 2 sigmoid(x . Wg[:, h]) in fp64, the 32 channels in order (the prefill gate's order)
+                const __nv_bfloat16* xr = p.gate_x + (long long)b * 32;
+                double z = 0.0;
+#pragma unroll
+                for (int cc = 0; cc < 32; ++cc)
+                    z = fma((double)__bfloat162float(xr[cc]), (double)__bfloat162float(p.Wg[cc * Hkv + h]), z);
+                const double g = 2.0 / (1.0 + exp(-z));
+                gw.x = (float)g;
+                gw.y = (float)(g - (double)gw.x);
+            }
+        }
+    }
+
+    // qhat's (or khat's) features 4 c .. and D/2 + 4 c .. in o0, o1.
+    __device__ __forceinline__ void finish(const Kv8TokenParams& p, int pos, int c, const float4* s_tab32,
+                                           const double2* s_tab64, uint2& o0, uint2& o1) {
+        constexpr int TPR = D / 8, HALF = D / 2;
+        const int i0 = 4 * c;
+        float4 cs4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cs4[e] = s_tab32[i0 + e];
+        rope_rms_exact4<D>(x0, x1, cs4, s_tab64 + i0, p.eps, o0, o1);
+        if (kind == kKeyValue && p.ve != nullptr) {
+            const double g64 = (double)gw.x + (double)gw.y;
+            v0 = gated_add4(v0, e0, gw.x, gw.y, g64);
+            v1 = gated_add4(v1, e1, gw.x, gw.y, g64);
+        }
+        const int off = pos & ((1 << p.c.log_p) - 1);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint2 y0 = u == 0 ? o0 : v0, y1 = u == 0 ? o1 : v1;
+            uint32_t a = max_half(max_abs2(max_abs2(max_abs2(max_abs2(0u, y0.x), y0.y), y1.x), y1.y));
+#pragma unroll
+            for (int d = TPR / 2; d >= 1; d >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
+            __syncwarp();
+            if (kind != kKeyValue || page < 0) continue;
+            int e = scale_exponent(a);
+            const long long ph = (long long)page * p.c.Hkv + h;
+            uint8_t* blk = (u == 0 ? p.c.k_cache : p.c.v_cache) + (ph << p.c.log_p) * D;
+            if (off > 0) {
+                const int old = exponent_of(old_scale[u]);
+                if (e > old) recode_rows<D>(blk, off, scale_of(max(old - e, -126)), 0, 1, c);
+                e = max(e, old);
+            }
+            const float inv = scale_of(-e);
+            *reinterpret_cast<uint32_t*>(blk + (long long)off * D + i0) = encode4(y0.x, y0.y, inv);
+            *reinterpret_cast<uint32_t*>(blk + (long long)off * D + HALF + i0) = encode4(y1.x, y1.y, inv);
+            if (c == 0) (u == 0 ? p.c.k_scale : p.c.v_scale)[ph] = scale_of(e);
+        }
+    }
+};
+
 // Rows of request b = blockIdx.x: its H query rows, then its Hkv key/value rows (when the token is to be
-// appended), D/8 lanes a row; blockIdx.y takes one group of 256 / (D/8) rows.  The RoPE row of the
-// token's position is built in shared memory by every block, in the split of the prefill table.
+// appended); blockIdx.y takes one group of 256 / (D/8) rows.  Every block builds the RoPE row of the token's
+// position in shared memory.
 template <int D>
 __global__ void __launch_bounds__(256) kv8_token_kernel(const Kv8TokenParams p) {
     constexpr int TPR = D / 8, HALF = D / 2, RPB = 256 / TPR;
     __shared__ float4 s_tab32[HALF];
     __shared__ double2 s_tab64[HALF];
-    const int b = (int)blockIdx.x;
-    const int Hkv = p.c.Hkv;
-    const int n = kv8_length(p.seq_len, b, p.max_pages, p.c.log_p);
-    const bool append = p.k != nullptr;
     grid_dependents_launch();     // the attention kernel may start: it waits before it reads what is written here
+    const int b = (int)blockIdx.x;
     if (b == 0 && blockIdx.y == 0)
         for (int i = threadIdx.x; i < p.n_counters; i += 256) p.counters[i] = 0;
+    const int n = kv8_length(p.seq_len, b, p.max_pages, p.c.log_p);
     if (n == 0) {
         if (blockIdx.y == 0) {
             if (threadIdx.x == 0 && p.seq_len[b] > 0) record_error(kErrIndex, kSiteKvLen);
-            for (int i = threadIdx.x; i < p.H * TPR; i += 256)
-                reinterpret_cast<uint4*>(p.out + (long long)b * p.H * D)[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (p.lse != nullptr)
-                for (int i = threadIdx.x; i < p.H; i += 256) p.lse[(long long)b * p.H + i] = -INFINITY;
+            kv8_empty_row<D>(p.out, p.lse, (long long)b * p.H, p.H);
         }
         return;
     }
-    const int pos = n - 1;
-    if ((int)threadIdx.x < HALF) {
-        const int i = (int)threadIdx.x;
-        const double theta = pow(p.base, -2.0 * (double)i / (double)D);
-        double sn, cs;
-        sincos((double)pos * theta, &sn, &cs);
-        float c_hi, c_lo, s_hi, s_lo;
-        rope_split(cs, c_hi, c_lo);
-        rope_split(sn, s_hi, s_lo);
-        s_tab32[i] = make_float4(c_hi, c_lo, s_hi, s_lo);
-        s_tab64[i] = make_double2(cs, sn);
-    }
-    // this thread's row, its inputs loaded before the barrier
-    const int row = (int)blockIdx.y * RPB + (int)threadIdx.x / TPR;
-    const int c = (int)threadIdx.x % TPR, i0 = 4 * c;
-    const bool is_q = row < p.H;
-    const int hk = row - p.H;
-    const bool is_kv = !is_q && append && hk < Hkv;
-    uint2 x0 = make_uint2(0u, 0u), x1 = x0, v0 = x0, v1 = x0, e0 = x0, e1 = x0;
-    float2 gw = make_float2(0.f, 0.f);
-    int page = -1;
-    float old_scale[2] = {1.f, 1.f};
-    if (is_q || is_kv) {
-        const __nv_bfloat16* src = is_q ? p.q + ((long long)b * p.H + row) * D : p.k + ((long long)b * Hkv + hk) * D;
-        x0 = ldg_stream8(src + i0);
-        x1 = ldg_stream8(src + HALF + i0);
-    }
-    if (is_kv) {
-        const __nv_bfloat16* vr = p.v + ((long long)b * Hkv + hk) * D;
-        v0 = ldg_stream8(vr + i0);
-        v1 = ldg_stream8(vr + HALF + i0);
-        page = __ldg(p.table + (long long)b * p.max_pages + (pos >> p.c.log_p));
-        if (page < 0 || page >= p.c.n_pages) {
-            if (c == 0) record_error(kErrIndex, kSiteKvPage);
-            page = -1;
-        } else {
-            old_scale[0] = p.c.k_scale[(long long)page * Hkv + hk];
-            old_scale[1] = p.c.v_scale[(long long)page * Hkv + hk];
-        }
-        if (p.ve != nullptr) {
-            const __nv_bfloat16* er = p.ve + ((long long)b * Hkv + hk) * D;
-            e0 = ldg_stream8(er + i0);
-            e1 = ldg_stream8(er + HALF + i0);
-            // 2 sigmoid(x . Wg[:, h]) in fp64, the 32 channels in order (the prefill gate's order)
-            const __nv_bfloat16* xr = p.gate_x + (long long)b * 32;
-            double z = 0.0;
-#pragma unroll
-            for (int cc = 0; cc < 32; ++cc)
-                z = fma((double)__bfloat162float(xr[cc]), (double)__bfloat162float(p.Wg[cc * Hkv + hk]), z);
-            const double g = 2.0 / (1.0 + exp(-z));
-            gw.x = (float)g;
-            gw.y = (float)(g - (double)gw.x);
-        }
-    }
+    const int row = (int)blockIdx.y * RPB + (int)threadIdx.x / TPR, c = (int)threadIdx.x % TPR;
+    const bool is_q = row < p.H, is_kv = !is_q && p.k != nullptr && row - p.H < p.c.Hkv;
+    Kv8Row<D> r;
+    r.load(p, b, n - 1, is_q ? kQuery : is_kv ? kKeyValue : kNoRow, is_q ? row : row - p.H, c);
+    if ((int)threadIdx.x < HALF) kv8_rope_entry<D>(p.base, n - 1, (int)threadIdx.x, s_tab32, s_tab64);
     __syncthreads();
-    float4 cs4[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) cs4[e] = s_tab32[i0 + e];
     uint2 o0, o1;
-    rope_rms_exact4<D>(x0, x1, cs4, s_tab64 + i0, p.eps, o0, o1);
+    r.finish(p, n - 1, c, s_tab32, s_tab64, o0, o1);
     if (is_q) {
-        __nv_bfloat16* dst = p.qh + ((long long)b * p.H + row) * D;
-        *reinterpret_cast<uint2*>(dst + i0) = o0;
-        *reinterpret_cast<uint2*>(dst + HALF + i0) = o1;
-    }
-    if (is_kv && p.ve != nullptr) {
-        const double g64 = (double)gw.x + (double)gw.y;
-        v0 = gated_add4(v0, e0, gw.x, gw.y, g64);
-        v1 = gated_add4(v1, e1, gw.x, gw.y, g64);
-    }
-    const int off = pos & ((1 << p.c.log_p) - 1);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const uint2 y0 = u == 0 ? o0 : v0, y1 = u == 0 ? o1 : v1;
-        uint32_t a = max_half(max_abs2(max_abs2(max_abs2(max_abs2(0u, y0.x), y0.y), y1.x), y1.y));
-#pragma unroll
-        for (int d = TPR / 2; d >= 1; d >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
-        __syncwarp();
-        if (!is_kv || page < 0) continue;
-        int e = scale_exponent(a);
-        const long long ph = (long long)page * Hkv + hk;
-        uint8_t* blk = (u == 0 ? p.c.k_cache : p.c.v_cache) + (ph << p.c.log_p) * D;
-        if (off > 0) {
-            const int old = exponent_of(old_scale[u]);
-            if (e > old) recode_rows<D>(blk, off, scale_of(max(old - e, -126)), 0, 1, c);
-            e = max(e, old);
-        }
-        const float inv = scale_of(-e);
-        *reinterpret_cast<uint32_t*>(blk + (long long)off * D + i0) = encode4(y0.x, y0.y, inv);
-        *reinterpret_cast<uint32_t*>(blk + (long long)off * D + HALF + i0) = encode4(y1.x, y1.y, inv);
-        if (c == 0) (u == 0 ? p.c.k_scale : p.c.v_scale)[ph] = scale_of(e);
+        __nv_bfloat16* dst = p.qh + ((long long)b * p.H + row) * D + 4 * c;
+        *reinterpret_cast<uint2*>(dst) = o0;
+        *reinterpret_cast<uint2*>(dst + HALF) = o1;
     }
 }
 
@@ -196,6 +231,9 @@ constexpr int kKv8Tiles = kKv8Chunk / 16;
 constexpr int kKv8Sms = 148;
 // Blocks of the attention kernel, at most: two per SM where a warp has one group of eight heads, else one.
 __host__ __device__ constexpr int kv8_max_blocks(int G) { return G <= 8 ? 2 * kKv8Sms : kKv8Sms; }
+constexpr int kKv8MinShare = 4;         // units of a block, where there are few
+constexpr int kKv8StepChunks = 8;       // chunks of a block in the one-launch form, at most
+constexpr int kKv8Whole = 4;            // items of at most so many units are not split
 constexpr float kSlack = 10.f;          // fp16 holds 2^15
 
 enum : unsigned int { kSiteKv8Full = 83, kSiteKv8Empty = 84 };
@@ -225,8 +263,11 @@ struct Kv8Cfg {
     static constexpr int SETS = KSLOTS / kKv8Tiles;              // chunks in work at a time
     static constexpr int TENSOR = kKv8Chunk * D;                 // bytes of a chunk's K (and V)
     static constexpr int HEADS = 8 * NT;                         // query heads of a warp
-    // results of half of the warps (the other half's are added in registers first)
-    static constexpr int MERGE = CONSUMERS / 2 * HEADS * D * 4;
+    // results of half of the warps (the other half's are added in registers first); later 4 KB of sums and the
+    // factors of an item's pieces
+    static constexpr int MERGE0 = CONSUMERS / 2 * HEADS * D * 4;
+    static constexpr int MERGE1 = 4096 + kKv8Sms * BLOCKS_PER_SM * HEADS * NRG * 4;
+    static constexpr int MERGE = MERGE0 > MERGE1 ? MERGE0 : MERGE1;
     // Ring stages; a multiple of SETS, so that a set of warps takes every use of its stages and its waits see each
     // phase of their barriers in turn.
     static constexpr int NS = NT == 1 ? (D == 128 ? 4 : 10) : (D == 128 ? 8 : 12);
@@ -273,9 +314,15 @@ struct Kv8Walk {
     }
 };
 
-// The block that has unit u of n units shared by m blocks: block c has [n c / m, n (c + 1) / m).
-__device__ __forceinline__ int kv8_owner(int u, int n, int m) { return (int)((((unsigned long long)u + 1) * m - 1) / (unsigned)n); }
-__device__ __forceinline__ int kv8_first_unit(int c, int n, int m) { return (int)((unsigned long long)n * c / (unsigned)m); }
+// n units in m equal stretches (the first n % m one longer): where stretch c begins, and which has unit u.
+struct Kv8Shares {
+    int m, q, r;
+    __device__ __forceinline__ Kv8Shares(int n, int blocks) : m(blocks), q(n / blocks), r(n % blocks) {}
+    __device__ __forceinline__ int begin(int c) const { return c * q + min(c, r); }
+    __device__ __forceinline__ int owner(int u) const {
+        return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q;
+    }
+};
 
 __device__ __forceinline__ uint32_t fp8x2_to_half2(uint32_t two) {
     uint32_t r;
@@ -424,35 +471,300 @@ __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0
     }
 }
 
+// Four features of the result, and its log-sum-exp: O / L, or an empty row where no key was visible (all on pages
+// outside the cache); a NaN stays one.
+template <int D>
+__device__ __forceinline__ void kv8_store4(const Kv8AttnParams& p, int b, int hk, int h, int d4, const float4& O, float M,
+                                           float L) {
+    const long long row = (long long)b * p.H + (long long)hk * p.G + h;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    *reinterpret_cast<uint2*>(p.out + row * D + 4 * d4) =
+        make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
+    if (d4 == 0 && p.lse != nullptr) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
 __device__ __forceinline__ void kv8_consumers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// tm_k, tm_v: the caches as {D, n_pages * Hkv * P} bytes, box {D, min(P, 64)}.
+// Shared memory of a block.
+template <class C>
+struct Kv8Shared {
+    uint8_t* ring;             // stage s: K at 2 s TENSOR, V behind it
+    float* o;
+    float* m;
+    float* l;
+    uint2* q;
+    float4* meta;
+    uint64_t* full;
+    uint64_t* empty;
+
+    __device__ __forceinline__ explicit Kv8Shared(uint8_t* dsmem) {
+        ring = dsmem + ((1024u - (smem_u32(dsmem) & 1023u)) & 1023u);
+        o = reinterpret_cast<float*>(ring + C::OFF_O);
+        m = reinterpret_cast<float*>(ring + C::OFF_ML);
+        l = m + C::CONSUMERS * C::HEADS;
+        q = reinterpret_cast<uint2*>(ring + C::OFF_Q);
+        meta = reinterpret_cast<float4*>(ring + C::OFF_META);
+        full = reinterpret_cast<uint64_t*>(ring + C::OFF_BAR);
+        empty = full + C::NS;
+    }
+    __device__ __forceinline__ void init_barriers() const {
+        for (int s = 0; s < C::NS; ++s) {
+            mbar_init(smem_u32(full + s), 2);
+            mbar_init(smem_u32(empty + s), C::CONSUMERS / C::SETS);
+        }
+        fence_barrier_init();
+    }
+};
+
+// The producer warp: the chunks of units [u0, u1) from walk position w into the ring.  box {D, min(P, 64)}.
+// kAppend: the block itself writes the new token (the threads that do so arrive at barrier 2), so the item's last chunk
+// waits for that.
+template <int D, class C, bool kAppend>
+__device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Kv8AttnParams& p,
+                                            const Kv8Shared<C>& sh, Kv8Walk w, int u0, int u1, int lane, bool append) {
+    // A box is a page, or the half of a 128-token page that a chunk has.
+    const int box_log = min(p.c.log_p, 6), nb_log = 6 - box_log;   // 64 >> nb_log keys; boxes of a chunk
+    const int tiles = (1 << box_log) / 16;
+    const uint32_t box_bytes = (uint32_t)((1 << box_log) * D);
+    // A batch: the boxes, one to a lane, of up to 32 >> nb_log chunks of an item.
+    struct Batch {
+        int chunks, hk, page, sub;     // this lane's table entry (kNone: not wanted), its first row in the page
+    };
+    constexpr int kNone = INT_MIN;
+    int u = u0, c = w.ch0 + (u0 - w.begin);
+    auto look_up = [&]() {
+        Batch f{0, w.hk, kNone, 0};
+        if (u >= u1) return f;
+        const int c_end = w.ch0 + (min(u1, w.begin + w.nch) - w.begin);
+        f.chunks = min(32 >> nb_log, c_end - c);
+        const long long pos = (long long)c * kKv8Chunk + ((long long)lane << box_log);
+        f.sub = (int)pos & ((1 << p.c.log_p) - 1);
+        if (lane < (f.chunks << nb_log) && pos < w.n && pos + (1 << box_log) > w.lo) {
+            f.page = __ldg(p.table + (long long)w.b * p.max_pages + (int)(pos >> p.c.log_p));
+            if (f.page == kNone) f.page = -1;
+        }
+        u += f.chunks;
+        c += f.chunks;
+        if (c == c_end && u < u1) {
+            w.next(p);
+            c = w.ch0;
+        }
+        return f;
+    };
+    bool ok = true;
+    int i = 0;                                                 // chunks before this batch
+    Batch f = look_up();
+    if (!kAppend) {
+        // the new tokens' codes and scales
+        grid_dependency_wait();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+    }
+    while (f.chunks > 0 && ok) {
+        const Batch after = look_up();
+        const int ph = f.page * p.c.Hkv + f.hk;
+        const bool there = f.page >= 0 && f.page < p.c.n_pages;
+        if (!there && f.page != kNone) record_error(kErrIndex, kSiteKvPage);
+        const int row = there ? (ph << p.c.log_p) + f.sub : -1;
+        // The copies run ahead of the scales, by at most the ring; a stage is full when it has both.
+        int copied = 0, told = 0;
+        auto copy = [&]() {
+            const int s = (i + copied) % C::NS, rel = lane - (copied << nb_log);   // this lane's box within the chunk
+            const bool load = rel >= 0 && rel < (1 << nb_log) && row >= 0;
+            const uint32_t n_load = (uint32_t)__popc(__ballot_sync(0xffffffffu, load));
+            const uint32_t bar = smem_u32(sh.full + s);
+            if (lane == 0) mbar_arrive_expect_tx(bar, n_load * 2u * box_bytes);
+            __syncwarp();
+            if (load) {
+                const uint32_t dst = smem_u32(sh.ring) + (uint32_t)(2 * s) * C::TENSOR + (uint32_t)rel * box_bytes;
+                tma_load_2d(dst, &tm_k, bar, 0, row);
+                tma_load_2d(dst + C::TENSOR, &tm_v, bar, 0, row);
+            }
+            ++copied;
+        };
+        if (kAppend && append && after.chunks == 0) {
+            while (copied < f.chunks - 1 && i + copied < C::NS) copy();
+            asm volatile("bar.sync 2, %0;" ::"n"(C::THREADS) : "memory");
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+        }
+        float ks = 0.f, vs = 0.f;
+        if (there) {
+            ks = *(const volatile float*)(p.c.k_scale + ph);
+            vs = *(const volatile float*)(p.c.v_scale + ph);
+        }
+        while (told < f.chunks) {
+            while (copied < f.chunks && copied < told + C::NS) {
+                const int k = i + copied;
+                if (k >= C::NS) {
+                    const uint32_t bar = smem_u32(sh.empty + k % C::NS), parity = (uint32_t)((k / C::NS) - 1) & 1u;
+                    if (copied > told) {                       // scales wait to be passed on: do not wait here
+                        if (!__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) break;
+                    } else if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_limit_ns, kSiteKv8Empty))) {
+                        ok = false;
+                        break;
+                    }
+                }
+                copy();
+            }
+            if (!ok) break;
+            const int s = (i + told) % C::NS, rel = lane - (told << nb_log);
+            if (rel >= 0 && rel < (1 << nb_log))
+                for (int k = 0; k < tiles; ++k)
+                    sh.meta[s * kKv8Tiles + rel * tiles + k] = make_float4(ks * p.c1, row >= 0 ? vs : -1.f, log2f(vs), 0.f);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(sh.full + s));
+            ++told;
+        }
+        i += ok ? f.chunks : copied;
+        f = after;
+    }
+    if (!ok)   // the copies in flight end before the block does
+        for (int k = max(0, i - C::NS); k < i; ++k)
+            mbar_wait(smem_u32(sh.full + k % C::NS), (uint32_t)(k / C::NS) & 1u, p.wait_limit_ns, kSiteKv8Full);
+}
+
+// The consumer warps' work on chunks [c_begin, c_end) of w's item, stages from counter i on; then the warps' sums are
+// joined, and emit(h, d4, O, M, L) gets features 4 d4 .. of each head's sum, its reference and weight.
+template <int D, int NT, int NRG, class C, class Emit>
+__device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Shared<C>& sh, const Kv8Walk& w, int c_begin,
+                                          int c_end, int& i, bool& ok, int warp, int lane, Emit emit) {
+    constexpr int NSTEP = D / 16, VW = D / 32;
+    const int g = lane >> 2, t = lane & 3;
+    const int rg = warp % NRG, kslot = warp / NRG;             // set of heads, share of the keys
+    const int set = kslot / kKv8Tiles % C::SETS;
+    const int h_base = rg * C::HEADS;                          // this warp's first head in the group
+    const uint4* q_lane = reinterpret_cast<const uint4*>(sh.q) + rg * NT * (NSTEP / 2) * 32 + lane;
+    float o[NT][2 * VW][4];
+    float m[NT][2], l[NT][2];                                  // heads 2 t and 2 t + 1 of each group
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+        m[x][0] = m[x][1] = -INFINITY;
+        l[x][0] = l[x][1] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2 * VW; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[x][k][e] = 0.f;
+    }
+    for (int c = c_begin; c < c_end; ++c, ++i) {
+        if (C::SETS > 1 && i % C::SETS != set) continue;
+        const int s = i % C::NS;
+        if (ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(sh.full + s), (uint32_t)(i / C::NS) & 1u, p.wait_limit_ns,
+                                                     kSiteKv8Full)))
+            ok = false;
+        if (!ok) break;
+        {
+            const int tile = kslot % kKv8Tiles;
+            const int pos0 = c * kKv8Chunk + 16 * tile;
+            const float4 meta = sh.meta[s * kKv8Tiles + tile];
+            // not wanted: outside the visible keys, or on a page that is not there
+            if (pos0 + 16 > w.lo && pos0 < w.n && meta.y >= 0.f)
+                kv8_tile<D, NT>(sh.ring + (2 * s) * C::TENSOR + tile * 16 * D, C::TENSOR, pos0, w.lo, w.n, meta, q_lane, o, m,
+                                l, g, t);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(sh.empty + s));
+    }
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], d);
+    // place `at` of the buffer; heads past the group are left out
+    auto put = [&](int at) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int hc = 8 * x + 2 * t + e;
+                if (h_base + hc >= p.G) continue;
+                if (g == 0) {
+                    sh.m[at * C::HEADS + hc] = m[x][e];
+                    sh.l[at * C::HEADS + hc] = l[x][e];
+                }
+#pragma unroll
+                for (int k = 0; k < 2 * VW; ++k)
+                    *reinterpret_cast<float2*>(sh.o + (at * C::HEADS + hc) * D + 4 * VW * g + 2 * k) =
+                        make_float2(o[x][k][e], o[x][k][2 + e]);
+            }
+    };
+    const bool upper = warp >= C::CONSUMERS / 2;
+    if (upper) put(warp - C::CONSUMERS / 2);
+    kv8_consumers_sync();
+    if (!upper) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int hc = 8 * x + 2 * t + e;
+                if (h_base + hc >= p.G) continue;
+                const int at = warp * C::HEADS + hc;
+                const float m2 = sh.m[at], l2 = sh.l[at];
+                const float M = fmaxf(m[x][e], m2);
+                const float f1 = kv8_factor(m[x][e], l[x][e], M), f2 = kv8_factor(m2, l2, M);
+#pragma unroll
+                for (int k = 0; k < 2 * VW; ++k) {
+                    const float2 o2 = *reinterpret_cast<const float2*>(sh.o + at * D + 4 * VW * g + 2 * k);
+                    o[x][k][e] = o[x][k][e] * f1 + o2.x * f2;
+                    o[x][k][2 + e] = o[x][k][2 + e] * f1 + o2.y * f2;
+                }
+                m[x][e] = M;
+                l[x][e] = l[x][e] * f1 + l2 * f2;
+            }
+    }
+    __syncwarp();
+    if (!upper) put(warp);                 // where it has just read
+    kv8_consumers_sync();
+    for (int x = (int)threadIdx.x; x < p.G * (D / 4); x += 256) {
+        const int h = x / (D / 4), d4 = x % (D / 4);
+        const int r = h / C::HEADS, hc = h % C::HEADS;
+        constexpr int KH = C::KSLOTS / 2;
+        float M = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < KH; ++k) M = fmaxf(M, sh.m[(k * NRG + r) * C::HEADS + hc]);
+        float L = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < KH; ++k) {
+            const int at = (k * NRG + r) * C::HEADS + hc;
+            const float f = kv8_factor(sh.m[at], sh.l[at], M);
+            const float4 v = *reinterpret_cast<const float4*>(sh.o + at * D + 4 * d4);
+            L = fmaf(sh.l[at], f, L);
+            O.x = fmaf(v.x, f, O.x);
+            O.y = fmaf(v.y, f, O.y);
+            O.z = fmaf(v.z, f, O.z);
+            O.w = fmaf(v.w, f, O.w);
+        }
+        emit(h, d4, O, M, L);
+    }
+}
+
+// Place of four features (from f, a multiple of 4) of query head h among the products' B operands: groups of eight
+// heads, steps, lanes; the features are taken in the order of a key row's bytes in kv8_tile.
+template <int D>
+__device__ __forceinline__ int kv8_q_place(int h, int f) {
+    constexpr int PER = D / 4;                                  // features of a lane (t)
+    const int st = (f % PER) / 4;
+    return (((h >> 3) * (D / 32) + st / 2) * 32 + (h & 7) * 4 + f / PER) * 2 + (st & 1);
+}
+__device__ __forceinline__ uint2 bf16x4_to_half4(uint2 raw) {
+    return make_uint2(pack_half2(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u)),
+                      pack_half2(__uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)));
+}
+
+// tm_k, tm_v: the caches as {D, n_pages * Hkv * P} bytes.
 template <int D, int NT, int NRG>
 __global__ void __launch_bounds__(Kv8Cfg<D, NT, NRG>::THREADS, Kv8Cfg<D, NT, NRG>::BLOCKS_PER_SM)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const Kv8AttnParams p) {
     using C = Kv8Cfg<D, NT, NRG>;
-    constexpr int NSTEP = D / 16;                 // mma steps along the features
-    constexpr int VW = D / 32;                    // 32-bit words of a lane's features of one value row
     extern __shared__ __align__(1024) uint8_t dsmem[];
-    uint8_t* smem = dsmem + ((1024u - (smem_u32(dsmem) & 1023u)) & 1023u);
-    float* s_o = reinterpret_cast<float*>(smem + C::OFF_O);
-    float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
-    float* s_l = s_m + C::CONSUMERS * C::HEADS;
-    uint2* s_q = reinterpret_cast<uint2*>(smem + C::OFF_Q);
-    float4* s_meta = reinterpret_cast<float4*>(smem + C::OFF_META);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint64_t* empty = full + C::NS;
+    const Kv8Shared<C> sh(dsmem);
     __shared__ int s_warp_sum[C::CONSUMERS + 1];
-    __shared__ int s_before, s_first, s_last;
+    __shared__ int s_from[4], s_to, s_last;
 
     const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31u);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::NS; ++s) {
-            mbar_init(smem_u32(full + s), 1);
-            mbar_init(smem_u32(empty + s), C::CONSUMERS / C::SETS);
-        }
-        fence_barrier_init();
+        sh.init_barriers();
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
@@ -480,273 +792,251 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NT, NRG>::THREADS, Kv8Cfg<D, NT, NRG
         total += s_warp_sum[i];
     }
     const int n_units = total * p.c.Hkv;
-    const int n_blocks = min((int)gridDim.x, n_units);
+    const int n_blocks = min((int)gridDim.x, (n_units + kKv8MinShare - 1) / kKv8MinShare);
     if ((int)blockIdx.x >= n_blocks) return;
-    const int u0 = kv8_first_unit(blockIdx.x, n_units, n_blocks), u1 = kv8_first_unit(blockIdx.x + 1, n_units, n_blocks);
-    if (u0 >= (incl - mine) * p.c.Hkv && u0 < incl * p.c.Hkv) {
+    const Kv8Shares shares(n_units, n_blocks);
+    // Where this block's stretch begins and ends: a boundary inside a small item moves to that item's end.
+    const int r0 = shares.begin(blockIdx.x), r1 = shares.begin(blockIdx.x + 1);
+    if (blockIdx.x + 1 == n_blocks && threadIdx.x == 0) s_to = n_units;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const int r = side == 0 ? r0 : r1;
+        if (r >= incl * p.c.Hkv || r < (incl - mine) * p.c.Hkv) continue;
         int before = incl - mine;
         for (w.b = b_lo;; ++w.b) {
             w.load(p);
-            if (u0 < (before + w.nch) * p.c.Hkv) break;
+            if (r < (before + w.nch) * p.c.Hkv) break;
             before += w.nch;
         }
-        s_first = w.b;
-        s_before = before;
+        const int hk = (r - before * p.c.Hkv) / w.nch, begin = before * p.c.Hkv + hk * w.nch;
+        const int at = r > begin && w.nch <= kKv8Whole ? begin + w.nch : r;
+        if (side == 0) {
+            s_from[0] = w.b;
+            s_from[1] = hk;
+            s_from[2] = begin;
+            s_from[3] = at;
+        } else {
+            s_to = at;
+        }
     }
     __syncthreads();
-    w.b = s_first;
+    const int u0 = s_from[3], u1 = s_to;
+    if (u0 >= u1) return;
+    w.b = s_from[0];
+    w.hk = s_from[1];
+    w.begin = s_from[2];
     w.load(p);
-    w.hk = (u0 - s_before * p.c.Hkv) / w.nch;
-    w.begin = s_before * p.c.Hkv + w.hk * w.nch;
+    if (u0 == w.begin + w.nch) w.next(p);
 
     if (warp == C::CONSUMERS) {
-        // ------------------------------------------------------------------------------- producer
-        // A box is a page, or the half of a 128-token page that a chunk has.
-        const int box_log = min(p.c.log_p, 6), nb_log = 6 - box_log;   // 64 >> nb_log keys; boxes of a chunk
-        const int tiles = (1 << box_log) / 16;
-        const uint32_t box_bytes = (uint32_t)((1 << box_log) * D);
-        bool waited = false, ok = true;
-        int i = 0;
-        for (int u = u0; u < u1 && ok; w.next(p)) {
-            const int end = min(u1, w.begin + w.nch);
-            const int c_end = w.ch0 + (end - w.begin);
-            int c = w.ch0 + (u - w.begin);
-            u = end;
-            int base = 0, row = -1;                        // chunk of lane 0's box; this lane's box: its row in the cache
-            float ks = 0.f, vs = 0.f;
-            for (int left = 0; c < c_end; ++c, --left) {
-                if (left == 0) {
-                    // the boxes of the next 32 >> nb_log chunks
-                    left = 32 >> nb_log;
-                    base = c;
-                    const long long pos = (long long)c * kKv8Chunk + ((long long)lane << box_log);
-                    const int c_stop = min(c_end, c + left);
-                    row = -1;
-                    int page = -1;
-                    if (pos < min((long long)w.n, (long long)c_stop * kKv8Chunk) && pos + (1 << box_log) > w.lo) {
-                        page = __ldg(p.table + (long long)w.b * p.max_pages + (int)(pos >> p.c.log_p));
-                        if (page < 0 || page >= p.c.n_pages) {
-                            record_error(kErrIndex, kSiteKvPage);
-                            page = -1;
-                        }
-                    }
-                    // the last chunk holds the new token, which the token kernel writes
-                    if (!waited && (long long)c_stop * kKv8Chunk >= w.n) {
-                        grid_dependency_wait();
-                        asm volatile("fence.proxy.async.global;" ::: "memory");
-                        waited = true;
-                    }
-                    if (page >= 0) {
-                        const int ph = page * p.c.Hkv + w.hk;
-                        ks = p.c.k_scale[ph];
-                        vs = p.c.v_scale[ph];
-                        row = (ph << p.c.log_p) + ((int)pos & ((1 << p.c.log_p) - 1));
-                    }
-                }
-                const int s = i % C::NS;
-                if (i >= C::NS && !__all_sync(0xffffffffu, mbar_wait(smem_u32(empty + s), (uint32_t)((i / C::NS) - 1) & 1u,
-                                                                     p.wait_limit_ns, kSiteKv8Empty))) {
-                    ok = false;
-                    break;
-                }
-                const int rel = lane - ((c - base) << nb_log);         // this lane's box within the chunk
-                const bool here = rel >= 0 && rel < (1 << nb_log);
-                const bool load = here && row >= 0;
-                if (here)
-                    for (int k = 0; k < tiles; ++k)
-                        s_meta[s * kKv8Tiles + rel * tiles + k] =
-                            make_float4(ks * p.c1, row >= 0 ? vs : -1.f, log2f(vs), 0.f);
-                const uint32_t n_load = (uint32_t)__popc(__ballot_sync(0xffffffffu, load));
-                const uint32_t bar = smem_u32(full + s);
-                if (lane == 0) mbar_arrive_expect_tx(bar, n_load * 2u * box_bytes);
-                __syncwarp();
-                if (load) {
-                    const uint32_t dst = smem_u32(smem) + (uint32_t)(2 * s) * C::TENSOR + (uint32_t)rel * box_bytes;
-                    tma_load_2d(dst, &tm_k, bar, 0, row);
-                    tma_load_2d(dst + C::TENSOR, &tm_v, bar, 0, row);
-                }
-                ++i;
-            }
-            if (u >= u1) break;
-        }
-        if (!ok)   // the copies in flight end before the block does
-            for (int k = max(0, i - C::NS); k < i; ++k)
-                mbar_wait(smem_u32(full + k % C::NS), (uint32_t)(k / C::NS) & 1u, p.wait_limit_ns, kSiteKv8Full);
+        kv8_produce<D, C, false>(tm_k, tm_v, p, sh, w, u0, u1, lane, false);
         return;
     }
-
-    // ----------------------------------------------------------------------------------- consumers
-    const int g = lane >> 2, t = lane & 3;
-    const int rg = warp % NRG, kslot = warp / NRG;             // set of heads, share of the keys
-    const int set = kslot / kKv8Tiles % C::SETS;
-    const int h_base = rg * C::HEADS;                          // this warp's first head in the group
-    const uint4* q_lane = reinterpret_cast<const uint4*>(s_q) + rg * NT * (NSTEP / 2) * 32 + lane;
     grid_dependency_wait();
     bool ok = true;
     int i = 0;
     for (int u = u0; u < u1;) {
         const int end = min(u1, w.begin + w.nch);
-        const int c_begin = w.ch0 + (u - w.begin), c_end = w.ch0 + (end - w.begin);
-        // qhat of the group's heads as the products' B operands: groups of eight heads, steps, lanes
-        for (int x = (int)threadIdx.x; x < C::NTG * NSTEP * 32; x += 256) {
-            const int xl = x & 31, st = (x >> 5) % NSTEP, hg = 8 * (x / (32 * NSTEP)) + (xl >> 2);
-            const int f = (D == 128 ? 32 : 16) * (xl & 3) + 4 * st;    // features in the order of a key row's bytes
+        for (int x = (int)threadIdx.x; x < C::NTG * 8 * (D / 4); x += 256) {
+            const int h = x / (D / 4), f = 4 * (x % (D / 4));
             uint2 raw = make_uint2(0u, 0u);
-            if (hg < p.G)
-                raw = *reinterpret_cast<const uint2*>(p.qh + ((long long)w.b * p.H + (long long)w.hk * p.G + hg) * D + f);
-            s_q[((x >> 5) / 2 * 32 + xl) * 2 + (st & 1)] =
-                make_uint2(pack_half2(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u)),
-                           pack_half2(__uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)));
+            if (h < p.G)
+                raw = *reinterpret_cast<const uint2*>(p.qh + ((long long)w.b * p.H + (long long)w.hk * p.G + h) * D + f);
+            sh.q[kv8_q_place<D>(h, f)] = bf16x4_to_half4(raw);
         }
         kv8_consumers_sync();              // and the last piece's results have been read
-        float o[NT][2 * VW][4];
-        float m[NT][2], l[NT][2];                              // heads 2 t and 2 t + 1 of each group
-#pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            m[x][0] = m[x][1] = -INFINITY;
-            l[x][0] = l[x][1] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 2 * VW; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[x][k][e] = 0.f;
-        }
-
-        for (int c = c_begin; c < c_end; ++c, ++i) {
-            if (C::SETS > 1 && i % C::SETS != set) continue;
-            const int s = i % C::NS;
-            if (ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(full + s), (uint32_t)(i / C::NS) & 1u, p.wait_limit_ns,
-                                                         kSiteKv8Full)))
-                ok = false;
-            if (!ok) break;
-            {
-                const int tile = kslot % kKv8Tiles;
-                const int pos0 = c * kKv8Chunk + 16 * tile;
-                const float4 meta = s_meta[s * kKv8Tiles + tile];
-                // not wanted: outside the visible keys, or on a page that is not there
-                if (pos0 + 16 > w.lo && pos0 < w.n && meta.y >= 0.f)
-                    kv8_tile<D, NT>(smem + (2 * s) * C::TENSOR + tile * 16 * D, C::TENSOR, pos0, w.lo, w.n, meta, q_lane, o, m, l,
-                                    g, t);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(empty + s));
-        }
-
-        // The piece's result: the warps' sums joined.
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], d);
-        // warp `at` of the buffer; heads past the group are left out
-        auto put = [&](int at) {
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int hc = 8 * x + 2 * t + e;
-                    if (h_base + hc >= p.G) continue;
-                    if (g == 0) {
-                        s_m[at * C::HEADS + hc] = m[x][e];
-                        s_l[at * C::HEADS + hc] = l[x][e];
-                    }
-#pragma unroll
-                    for (int k = 0; k < 2 * VW; ++k)
-                        *reinterpret_cast<float2*>(s_o + (at * C::HEADS + hc) * D + 4 * VW * g + 2 * k) =
-                            make_float2(o[x][k][e], o[x][k][2 + e]);
-                }
-        };
-        const bool upper = warp >= C::CONSUMERS / 2;
-        if (upper) put(warp - C::CONSUMERS / 2);
-        kv8_consumers_sync();
-        if (!upper) {
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int hc = 8 * x + 2 * t + e;
-                    if (h_base + hc >= p.G) continue;
-                    const int at = warp * C::HEADS + hc;
-                    const float m2 = s_m[at], l2 = s_l[at];
-                    const float M = fmaxf(m[x][e], m2);
-                    const float f1 = kv8_factor(m[x][e], l[x][e], M), f2 = kv8_factor(m2, l2, M);
-#pragma unroll
-                    for (int k = 0; k < 2 * VW; ++k) {
-                        const float2 o2 = *reinterpret_cast<const float2*>(s_o + at * D + 4 * VW * g + 2 * k);
-                        o[x][k][e] = o[x][k][e] * f1 + o2.x * f2;
-                        o[x][k][2 + e] = o[x][k][2 + e] * f1 + o2.y * f2;
-                    }
-                    m[x][e] = M;
-                    l[x][e] = l[x][e] * f1 + l2 * f2;
-                }
-        }
-        __syncwarp();
-        if (!upper) put(warp);             // where it has just read
-        kv8_consumers_sync();
         const bool alone = u == w.begin && end == w.begin + w.nch;
-        const int slot = 2 * (int)blockIdx.x + (u0 < w.begin ? 1 : 0);
-        for (int x = (int)threadIdx.x; x < p.G * D; x += 256) {
-            const int h = x / D, d = x % D;
-            const int r = h / C::HEADS, hc = h % C::HEADS;
-            constexpr int KH = C::KSLOTS / 2;
-            float M = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < KH; ++k) M = fmaxf(M, s_m[(k * NRG + r) * C::HEADS + hc]);
-            float L = 0.f, O = 0.f;
-#pragma unroll
-            for (int k = 0; k < KH; ++k) {
-                const int at = (k * NRG + r) * C::HEADS + hc;
-                const float f = kv8_factor(s_m[at], s_l[at], M);
-                L = fmaf(s_l[at], f, L);
-                O = fmaf(s_o[at * D + d], f, O);
-            }
-            if (alone) {
-                const long long row = (long long)w.b * p.H + (long long)w.hk * p.G + h;
-                // no visible key (pages outside the cache only): an empty row; a NaN stays one
-                p.out[row * D + d] = __float2bfloat16_rn(L == 0.f ? 0.f : O / L);
-                if (d == 0 && p.lse != nullptr) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-            } else {
-                float* pt = p.part + ((long long)slot * p.G + h) * (D + 4);
-                pt[d] = O;
-                if (d == 0) {
-                    pt[D] = M;
-                    pt[D + 1] = L;
-                }
-            }
-        }
+        const int slot = 2 * (int)blockIdx.x + (r0 < w.begin ? 1 : 0);
+        kv8_piece<D, NT, NRG, C>(p, sh, w, w.ch0 + (u - w.begin), w.ch0 + (end - w.begin), i, ok, warp, lane,
+                                 [&](int h, int d4, const float4& O, float M, float L) {
+                                     if (alone) {
+                                         kv8_store4<D>(p, w.b, w.hk, h, d4, O, M, L);
+                                     } else {
+                                         float* pt = p.part + ((long long)slot * p.G + h) * (D + 4);
+                                         *reinterpret_cast<float4*>(pt + 4 * d4) = O;
+                                         if (d4 == 0) *reinterpret_cast<float2*>(pt + D) = make_float2(M, L);
+                                     }
+                                 });
         if (!alone) {
-            const int c_first = kv8_owner(w.begin, n_units, n_blocks);
-            const int pieces = kv8_owner(w.begin + w.nch - 1, n_units, n_blocks) - c_first + 1;
+            const int c_first = shares.owner(w.begin);
+            const int pieces = shares.owner(w.begin + w.nch - 1) - c_first + 1;
             __threadfence();
             kv8_consumers_sync();
             if (threadIdx.x == 0) s_last = atomicAdd(p.counters + c_first, 1) == pieces - 1;
             kv8_consumers_sync();
             if (s_last) {
                 __threadfence();
-                const int first_slot = 2 * c_first + (kv8_first_unit(c_first, n_units, n_blocks) < w.begin ? 1 : 0);
-                for (int x = (int)threadIdx.x; x < p.G * D; x += 256) {
-                    const int h = x / D, d = x % D;
-                    auto at = [&](int k) {
-                        return p.part + ((long long)(k == 0 ? first_slot : 2 * (c_first + k)) * p.G + h) * (D + 4);
-                    };
-                    float M = -INFINITY, L = 0.f, O = 0.f;
-                    for (int k = 0; k < pieces; ++k) M = fmaxf(M, __ldcg(at(k) + D));
-                    for (int k = 0; k < pieces; ++k) {
-                        const float mk = __ldcg(at(k) + D), lk = __ldcg(at(k) + D + 1);
-                        const float f = kv8_factor(mk, lk, M);
-                        L = fmaf(lk, f, L);
-                        O = fmaf(__ldcg(at(k) + d), f, O);
+                const int first_slot = 2 * c_first + (shares.begin(c_first) < w.begin ? 1 : 0);
+                auto part = [&](int k, int h) {
+                    return p.part + ((long long)(k == 0 ? first_slot : 2 * (c_first + k)) * p.G + h) * (D + 4);
+                };
+                // each head's reference and sum, and every piece's factor: a warp per head, a lane per piece
+                float4* s_sum = reinterpret_cast<float4*>(sh.o);
+                float* s_f = sh.o + 1024;
+                for (int h = warp; h < p.G; h += C::CONSUMERS) {
+                    float M = -INFINITY, L = 0.f;
+                    for (int k = lane; k < pieces; k += 32) M = fmaxf(M, __ldcg(part(k, h) + D));
+#pragma unroll
+                    for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+                    for (int k = lane; k < pieces; k += 32) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(k, h) + D));
+                        const float f = kv8_factor(ml.x, ml.y, M);
+                        s_f[k * p.G + h] = f;
+                        L = fmaf(ml.y, f, L);
                     }
-                    const long long row = (long long)w.b * p.H + (long long)w.hk * p.G + h;
-                    p.out[row * D + d] = __float2bfloat16_rn(L == 0.f ? 0.f : O / L);
-                    if (d == 0 && p.lse != nullptr)
-                        p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+#pragma unroll
+                    for (int d = 16; d >= 1; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+                    if (lane == 0) {
+                        sh.m[h] = M;
+                        sh.l[h] = L;
+                    }
                 }
+                kv8_consumers_sync();
+                // four features to a thread; with few heads, several threads share the pieces
+                const int n_out = p.G * (D / 4), share = n_out < 256 ? 256 / n_out : 1;
+                for (int x = (int)threadIdx.x; x < n_out * share; x += 256) {
+                    const int ox = x % n_out, h = ox / (D / 4), d4 = ox % (D / 4);
+                    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int k = x / n_out; k < pieces; k += share) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part(k, h)) + d4);
+                        const float f = s_f[k * p.G + h];
+                        O.x = fmaf(v.x, f, O.x);
+                        O.y = fmaf(v.y, f, O.y);
+                        O.z = fmaf(v.z, f, O.z);
+                        O.w = fmaf(v.w, f, O.w);
+                    }
+                    if (share > 1) s_sum[x] = O;
+                    else kv8_store4<D>(p, w.b, w.hk, h, d4, O, sh.m[h], sh.l[h]);
+                }
+                if (share > 1) {
+                    kv8_consumers_sync();
+                    if ((int)threadIdx.x < n_out) {
+                        const int h = (int)threadIdx.x / (D / 4), d4 = (int)threadIdx.x % (D / 4);
+                        float4 O = s_sum[threadIdx.x];
+                        for (int k = 1; k < share; ++k) {
+                            const float4 v = s_sum[k * n_out + threadIdx.x];
+                            O.x += v.x;
+                            O.y += v.y;
+                            O.z += v.z;
+                            O.w += v.w;
+                        }
+                        kv8_store4<D>(p, w.b, w.hk, h, d4, O, sh.m[h], sh.l[h]);
+                    }
+                }
+                kv8_consumers_sync();      // before the buffer is written again
             }
         }
         u = end;
         if (u < u1) w.next(p);
     }
+}
+
+// The step in one launch, for calls with few items: a cluster of blocks per (request, key/value head), each taking an
+// equal share of the item's chunks (pages of at most a chunk: the new token's page, whose scale it may change, is then
+// in the last chunk alone).  While the first codes load, every block forms qhat of its group's heads itself, and the
+// one with the last chunk puts the new token into the cache; the blocks' sums are joined through distributed shared memory.
+// Against the two kernels: no dependent launch and nothing in global memory between the blocks (a d24 request of
+// 301 tokens 9 -> 7 us), but the split follows each item alone, so the GPU is not shared evenly by many ragged ones.
+template <int D>
+__global__ void __launch_bounds__(Kv8Cfg<D, 1, 1>::THREADS, 2)
+    kv8_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Kv8AttnParams p,
+                    const Kv8TokenParams tk) {
+    using C = Kv8Cfg<D, 1, 1>;
+    constexpr int TPR = D / 8, HALF = D / 2;
+    extern __shared__ __align__(1024) uint8_t dsmem[];
+    const Kv8Shared<C> sh(dsmem);
+    __shared__ float4 s_tab32[HALF];
+    __shared__ double2 s_tab64[HALF];
+    __shared__ __align__(16) float s_part[8 * (D + 4)];        // this block's sums: [head][O, then M and L]
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31u);
+    const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
+    const int item = (int)blockIdx.x / ranks;
+    Kv8Walk w;
+    w.b = item / p.c.Hkv;
+    w.hk = item - w.b * p.c.Hkv;
+    w.begin = 0;
+    w.load(p);
+    if (w.n == 0) {                                            // every block of the cluster alike
+        if (rank == 0) {
+            if (threadIdx.x == 0 && w.hk == 0 && p.seq_len[w.b] > 0) record_error(kErrIndex, kSiteKvLen);
+            kv8_empty_row<D>(p.out, p.lse, (long long)w.b * p.H + w.hk * p.G, p.G);
+        }
+        return;
+    }
+    if (threadIdx.x == 0) sh.init_barriers();
+    __syncthreads();
+    const int share = (w.nch + ranks - 1) / ranks;
+    const int u0 = min(w.nch, rank * share), u1 = min(w.nch, u0 + share);
+    const bool append = tk.k != nullptr && u0 < u1 && u1 == w.nch;
+    if (warp == C::CONSUMERS) {
+        kv8_produce<D, C, true>(tm_k, tm_v, p, sh, w, u0, u1, lane, append);
+    } else {
+        const int row = (int)threadIdx.x / TPR, c = (int)threadIdx.x % TPR;
+        Kv8Row<D> r;
+        r.load(tk, w.b, w.n - 1, row < p.G ? kQuery : row == p.G && append ? kKeyValue : kNoRow,
+               row < p.G ? w.hk * p.G + row : w.hk, c);
+        if ((int)threadIdx.x < HALF) kv8_rope_entry<D>(tk.base, w.n - 1, (int)threadIdx.x, s_tab32, s_tab64);
+        kv8_consumers_sync();
+        uint2 o0, o1;
+        r.finish(tk, w.n - 1, c, s_tab32, s_tab64, o0, o1);
+        if (append) {
+            __threadfence();
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            asm volatile("bar.arrive 2, %0;" ::"n"(C::THREADS) : "memory");
+        }
+        if (row < 8) {
+            const bool head = row < p.G;
+            sh.q[kv8_q_place<D>(row, 4 * c)] = head ? bf16x4_to_half4(o0) : make_uint2(0u, 0u);
+            sh.q[kv8_q_place<D>(row, HALF + 4 * c)] = head ? bf16x4_to_half4(o1) : make_uint2(0u, 0u);
+        }
+        kv8_consumers_sync();
+        bool ok = true;
+        int i = 0;
+        kv8_piece<D, 1, 1, C>(p, sh, w, w.ch0 + u0, w.ch0 + u1, i, ok, warp, lane,
+                              [&](int h, int d4, const float4& O, float M, float L) {
+                                  if (ranks == 1) {
+                                      kv8_store4<D>(p, w.b, w.hk, h, d4, O, M, L);
+                                  } else {
+                                      float* pt = s_part + h * (D + 4);
+                                      *reinterpret_cast<float4*>(pt + 4 * d4) = O;
+                                      if (d4 == 0) *reinterpret_cast<float2*>(pt + D) = make_float2(M, L);
+                                  }
+                              });
+    }
+    if (ranks == 1) return;
+    __syncwarp();
+    cluster_sync_all();
+    // the outputs, dealt over the blocks
+    const int n_out = p.G * (D / 4);
+    for (int x = rank * C::THREADS + (int)threadIdx.x; x < n_out; x += ranks * C::THREADS) {
+        const int h = x / (D / 4), d4 = x % (D / 4);
+        const float* pt = s_part + h * (D + 4);
+        float mk[kDecodeMaxCluster], lk[kDecodeMaxCluster];
+        float M = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kDecodeMaxCluster; ++k) {
+            if (k >= ranks) break;
+            mk[k] = ld_shared_cluster_f32(pt + D, k);
+            lk[k] = ld_shared_cluster_f32(pt + D + 1, k);
+            M = fmaxf(M, mk[k]);
+        }
+        float L = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kDecodeMaxCluster; ++k) {
+            if (k >= ranks) break;
+            const float f = kv8_factor(mk[k], lk[k], M);
+            L = fmaf(lk[k], f, L);
+            O.x = fmaf(ld_shared_cluster_f32(pt + 4 * d4, k), f, O.x);
+            O.y = fmaf(ld_shared_cluster_f32(pt + 4 * d4 + 1, k), f, O.y);
+            O.z = fmaf(ld_shared_cluster_f32(pt + 4 * d4 + 2, k), f, O.z);
+            O.w = fmaf(ld_shared_cluster_f32(pt + 4 * d4 + 3, k), f, O.w);
+        }
+        kv8_store4<D>(p, w.b, w.hk, h, d4, O, M, L);
+    }
+    // the blocks keep their shared memory until all have read it
+    cluster_sync_all();
 }
 
 }  // namespace swa

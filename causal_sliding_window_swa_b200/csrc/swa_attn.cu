@@ -1443,12 +1443,57 @@ int launch_kv8_attention_n(int dev, const CUtensorMap& tk, const CUtensorMap& tv
     return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
+// The step as one launch (kv8_step_kernel), clusters of `ranks` blocks.
 template <int D>
-int launch_kv8_attention(int dev, const swa::Kv8AttnParams& a, cudaStream_t st) {
+int launch_kv8_step(int dev, const CUtensorMap& tk, const CUtensorMap& tv, const swa::Kv8AttnParams& a,
+                    const swa::Kv8TokenParams& t, int ranks, cudaStream_t st) {
+    using C = swa::Kv8Cfg<D, 1, 1>;
+    static std::once_flag once[64];
+    static bool ok[64] = {false};
+    std::call_once(once[dev], [&] {
+        ok[dev] = cudaFuncSetAttribute(swa::kv8_step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) ==
+                  cudaSuccess;
+    });
+    if (!ok[dev]) {
+        cudaGetLastError();
+        return SWA_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.B * a.c.Hkv * ranks));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, swa::kv8_step_kernel<D>, tk, tv, a, t) != cudaSuccess) {
+        cudaGetLastError();
+        return SWA_ERR_CUDA;
+    }
+    return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+template <int D>
+int launch_kv8_decode(int dev, const swa::Kv8AttnParams& a, const swa::Kv8TokenParams& t, cudaStream_t st) {
     CUtensorMap tk, tv;
     const long long rows = ((long long)a.c.n_pages * a.c.Hkv) << a.c.log_p;
     const int box = std::min(1 << a.c.log_p, swa::kKv8Chunk);
     if (!make_page_map(&tk, a.c.k_cache, rows, D, box) || !make_page_map(&tv, a.c.v_cache, rows, D, box)) return SWA_ERR_CUDA;
+    // One launch where pages do not pass a chunk, every item gets at least one of the resident blocks and the longest possible item leaves a
+    // block no more than kKv8StepChunks chunks.
+    const long long items = (long long)a.B * a.c.Hkv, slots = 2ll * std::min(g_num_sms[dev], swa::kKv8Sms);
+    const long long most = (long long)a.max_pages << a.c.log_p;
+    const long long chunks = std::min<long long>(most, a.W > 0 ? a.W : most) / swa::kKv8Chunk + 1;
+    const int ranks = (int)std::min<long long>(std::min<long long>(slots / std::max(1ll, items), swa::kDecodeMaxCluster), chunks);
+    if (a.G <= 8 && a.c.log_p <= 6 && ranks >= 1 && (chunks + ranks - 1) / ranks <= swa::kKv8StepChunks)
+        return launch_kv8_step<D>(dev, tk, tv, a, t, ranks, st);
+    const int rows_per_block = 256 / (D / 8);
+    const dim3 grid((unsigned)a.B, (unsigned)((a.H + (t.k ? a.c.Hkv : 0) + rows_per_block - 1) / rows_per_block));
+    swa::kv8_token_kernel<D><<<grid, 256, 0, st>>>(t);
     if (a.G <= 8) return launch_kv8_attention_n<D, 1, 1>(dev, tk, tv, a, st);
     if (a.G <= 16) return launch_kv8_attention_n<D, 2, 1>(dev, tk, tv, a, st);
     if (a.G <= 32) return launch_kv8_attention_n<D, 4, 1>(dev, tk, tv, a, st);
@@ -1501,14 +1546,10 @@ int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void*
                                 static_cast<const bf*>(ve), static_cast<const bf*>(gate_x), static_cast<const bf*>(Wg),
                                 block_table, seq_len, reinterpret_cast<bf*>(ws + L.qh), static_cast<bf*>(out), lse, c, H,
                                 max_pages, counters, swa::kv8_max_blocks(H / Hkv), (double)rope_base, (double)eps};
-    const int rows = 256 / (D / 8);
-    const dim3 tg((unsigned)B, (unsigned)((H + (k ? Hkv : 0) + rows - 1) / rows));
     const swa::Kv8AttnParams a{reinterpret_cast<const bf*>(ws + L.qh), block_table, seq_len, doc_start, static_cast<bf*>(out),
                                lse, c, counters, reinterpret_cast<float*>(ws + L.part), B, H, H / Hkv, max_pages,
                                std::max(0, window), (float)(1.4426950408889634 / std::sqrt((double)D)), wait_limit_ns()};
-    if (D == 128) swa::kv8_token_kernel<128><<<tg, 256, 0, st>>>(t);
-    else swa::kv8_token_kernel<64><<<tg, 256, 0, st>>>(t);
-    return D == 128 ? launch_kv8_attention<128>(dev, a, st) : launch_kv8_attention<64>(dev, a, st);
+    return D == 128 ? launch_kv8_decode<128>(dev, a, t, st) : launch_kv8_decode<64>(dev, a, t, st);
 }
 
 int swa_attn_selftest_wait(int limit_ms, swa_stream_t stream) {

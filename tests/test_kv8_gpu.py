@@ -238,7 +238,9 @@ class Batch:
         seq = kw.pop("seq_len", None)
         seq = i32(self.lens) if seq is None else seq
         k, v, ve, gx, wg = (self.k, self.v, self.ve, self.gate_x, self.Wg) if append else (None,) * 5
-        return swa.decode_kv8(self.q, k, v, *self.cache.all(), self.table.cuda(), seq, self.window, ve, gx, wg,
+        # a table for much longer requests: the call cannot count on short ones, and goes another way
+        table = torch.nn.functional.pad(self.table, (0, kw.pop("wide", 0)), value=-1)
+        return swa.decode_kv8(self.q, k, v, *self.cache.all(), table.cuda(), seq, self.window, ve, gx, wg,
                               doc_start=None if self.start is None else i32(self.start), **kw)
 
     def token(self, b):
@@ -291,16 +293,19 @@ CASES = [
     ([200, 600], 64, 1, 128, 16, 0, False, False),          # 64
     ([150] * 40, 5, 5, 64, 64, 128, False, False),
     ([3000, 2999, 10, 2048], 12, 12, 128, 64, 1024, True, False),
+    ([449, 500, 512, 1], 4, 4, 128, 128, 300, True, False),
     ([5000], 2, 1, 128, 128, 0, False, False),
     ([257 + 13 * i for i in range(30)], 6, 3, 64, 32, 0, False, True),
 ]
 
 
+@pytest.mark.parametrize("wide", [0, 4096])
 @pytest.mark.parametrize("case", CASES, ids=[f"{len(c[0])}x{max(c[0])} H{c[1]}/{c[2]} D{c[3]} P{c[4]} W{c[5]}" for c in CASES])
-def test_decode_matches_the_plain_statement(case):
+def test_decode_matches_the_plain_statement(case, wide):
     lens, H, Hkv, D, P, window, ve, doc = case
+    window = window or (1 << 30 if wide else 0)
     x = Batch(lens, H, Hkv, D, P, window, seed=sum(lens) + H, ve=ve, doc=doc)
-    out, lse = x.run()
+    out, lse = x.run(wide=wide)
     x.append_plain()
     used = [x.token(b)[2] for b, n in enumerate(lens) if n > 0]
     x.cache.check([p * P + i for s in used for p, o in [divmod(s, P)] for i in range(o + 1)])
@@ -309,9 +314,9 @@ def test_decode_matches_the_plain_statement(case):
     o2, l2 = torch.full_like(out, float("nan")), torch.full_like(lse, float("nan"))
     ws = torch.full((swa.swa_attn_kv8_decode_workspace_bytes(len(lens), H, Hkv, D),), 255, dtype=torch.uint8, device="cuda")
     for _ in range(2):
-        x.run(append=False, out=o2, lse=l2, workspace=ws)
+        x.run(append=False, out=o2, lse=l2, workspace=ws, wide=wide)
         assert torch.equal(o2, out) and torch.equal(l2, lse)
-    o3, l3 = x.run()          # the same token again: it takes the place it has
+    o3, l3 = x.run(wide=wide)          # the same token again: it takes the place it has
     assert torch.equal(o3, out) and torch.equal(l3, lse)
     swa.check_device_status()
 
@@ -364,7 +369,8 @@ def test_decode_many_units_for_each_block(B, H, Hkv, D, P, window, most):
         assert (np.abs(f64(lse[b]) - ref_l) <= 2 * kv8_plain.lse_tolerance(ref_l, D)).all(), (b, n)
 
 
-def test_adversarial_scores_and_scales():
+@pytest.mark.parametrize("wide", [0, 4096])
+def test_adversarial_scores_and_scales(wide):
     # keys along the query and against it, so that probabilities span the whole range; values of very different size in
     # neighbouring pages
     H, D, P, n = 2, 128, 16, 200
@@ -378,16 +384,33 @@ def test_adversarial_scores_and_scales():
     vp[0, :64] = 0
     slots = torch.stack([torch.tensor([int(x.table[b, u // P]) * P + u % P for u in t]) for b in range(2)]).int().cuda()
     x.cache.write(kh, vp, slots.contiguous())
-    out, lse = x.run()
+    out, lse = x.run(wide=wide)
     x.append_plain()
     x.check(out, lse)
 
 
-def test_values_that_are_not_visible_do_not_matter():
+@pytest.mark.parametrize("wide", [0, 4096])
+@pytest.mark.parametrize("P", [16, 64, 128])
+def test_the_scale_of_the_last_page_grows_under_the_step(P, wide):
+    # new tokens far larger than what their pages hold: the codes that are there move to the new scale in the same step
+    x = Batch([P + P // 2 + 3, 2 * P, 5, P + 1], 4, 4, 128, P, 0, seed=P)
+    x.v *= 64
+    x.k *= 0
+    x.k[:, :, 0] = 8             # khat has one large element
+    out, lse = x.run(wide=wide)
+    before = x.cache.plain[1].e.copy()
+    x.append_plain()
+    assert (x.cache.plain[1].e > before).any()
+    x.cache.check([int(x.table[b, t // P]) * P + t % P for b, n in enumerate(x.lens) for t in range(n)])
+    x.check(out, lse)
+
+
+@pytest.mark.parametrize("wide", [0, 4096])
+def test_values_that_are_not_visible_do_not_matter(wide):
     # NaN codes and scales in pages outside the window, behind the last token, and in rows before the document start
     x = Batch([100, 77], 4, 2, 64, 16, 40, seed=3, doc=True)
     x.start = [70, 0]
-    out, lse = x.run()
+    out, lse = x.run(wide=wide)
     for b, n in enumerate(x.lens):
         lo = kv8_plain.visible(n, 40, x.start[b])
         for t in range(lo // 16 * 16, lo):
@@ -397,29 +420,30 @@ def test_values_that_are_not_visible_do_not_matter():
         for t in range(n, -(-n // 16) * 16):
             page, off = int(x.table[b, t // 16]), t % 16
             x.cache.v.view(torch.uint8)[page, :, off] = 0x7f
-    o2, l2 = x.run(append=False)
+    o2, l2 = x.run(append=False, wide=wide)
     assert torch.isfinite(out.float()).all() and torch.equal(out, o2) and torch.equal(lse, l2)
     # a NaN that is visible to one key/value head's queries stays with them
     lo = kv8_plain.visible(100, 40, 70)
     x.cache.v.view(torch.uint8)[int(x.table[0, lo // 16]), 1, lo % 16, 5] = 0x7f
-    o3, _ = x.run(append=False)
+    o3, _ = x.run(append=False, wide=wide)
     assert torch.isnan(o3[0, 2:, 5].float()).all()
     o3[0, 2:, 5] = out[0, 2:, 5]
     assert torch.equal(o3, out)
 
 
-def test_bad_pages_and_lengths_are_recorded_and_skipped():
+@pytest.mark.parametrize("wide", [0, 4096])
+def test_bad_pages_and_lengths_are_recorded_and_skipped(wide):
     x = Batch([90, 40, 33], 2, 2, 64, 16, 0, seed=4)
     swa.check_device_status()
     n_pages = x.cache.k.shape[0]
-    out, lse = x.run()
+    out, lse = x.run(wide=wide)
     x.append_plain()
     x.check(out, lse)
     swa.check_device_status()
     for bad in (-1, n_pages, 2 ** 31 - 1, -2 ** 31):
         was = int(x.table[0, 2])
         x.table[0, 2] = bad
-        out, lse = x.run(append=False)
+        out, lse = x.run(append=False, wide=wide)
         rc, detail = swa.swa_attn_last_device_status()
         assert rc == swa.SWA_ERR_INVALID_ARG and (detail >> 8) & 0xff == 81
         x.check(out, lse, bad_pages=(bad,))
@@ -428,23 +452,23 @@ def test_bad_pages_and_lengths_are_recorded_and_skipped():
     was = int(x.table[2, 2])
     x.table[2, 2] = n_pages
     before = x.cache.k.view(torch.uint8).clone()
-    out, lse = x.run()
+    out, lse = x.run(wide=wide)
     assert swa.swa_attn_last_device_status()[0] == swa.SWA_ERR_INVALID_ARG
     assert torch.equal(before, x.cache.k.view(torch.uint8))
     x.check(out, lse, bad_pages=(n_pages,))
     # no page at all: nothing is visible
     x.table[2, :] = -1
-    out, lse = x.run()
+    out, lse = x.run(wide=wide)
     assert swa.swa_attn_last_device_status()[0] == swa.SWA_ERR_INVALID_ARG
     assert (out[2] == 0).all() and (lse[2] == float("-inf")).all()
     # a length that the table cannot hold: an empty row
-    out, lse = x.run(append=False, seq_len=i32([90, 40, 16 * x.table.shape[1] + 1]))
+    out, lse = x.run(append=False, wide=wide, seq_len=i32([90, 40, 16 * (x.table.shape[1] + wide) + 1]))
     rc, detail = swa.swa_attn_last_device_status()
     assert rc == swa.SWA_ERR_INVALID_ARG and (detail >> 8) & 0xff == 82
     assert (out[2] == 0).all() and (lse[2] == float("-inf")).all()
     x.table[2, 2] = was
     # negative lengths are empty rows too, and nothing to record
-    out, lse = x.run(append=False, seq_len=i32([90, -7, -2 ** 31]))
+    out, lse = x.run(append=False, wide=wide, seq_len=i32([90, -7, -2 ** 31]))
     swa.check_device_status()
     assert (out[1:] == 0).all() and (lse[1:] == float("-inf")).all()
 
