@@ -607,31 +607,52 @@ def forward_x(x, Wqkv, H: int, Hkv: int, D: int, window: int = 0, ve=None, Wg=No
     return out, lse
 
 
+# The calls below run once per layer and token, so their host time counts: each check costs a fraction of a
+# microsecond, and only one that fails goes through _want, which says what is wrong.
+
+def _check_all(dev, checks):
+    """checks: (name, tensor, shape, dtype).  Every tensor must be contiguous, of that shape and dtype, on `dev`."""
+    index = dev.index if dev.type == "cuda" else -2
+    for name, t, shape, dtype in checks:
+        if t is None or not (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+            _want(name, t, shape, dtype, dev)
+
+
+class _NoContext:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return None
+
+
+_NO_CONTEXT = _NoContext()
+
+
 def _on_stream(stream, dev):
     """Context in which the current device is `dev` and the current stream the one the call runs on
     (`stream`: a torch stream on that device, a raw handle, or None for the device's current stream), so
     that what the call allocates belongs to that stream; and the stream's handle."""
     import torch
     if stream is None:
-        return torch.cuda.device(dev), torch.cuda.current_stream(dev).cuda_stream
+        index = dev.index
+        handle = torch._C._cuda_getCurrentRawStream(index)
+        return (_NO_CONTEXT if torch.cuda.current_device() == index else torch.cuda.device(dev)), handle
     handle = _stream_handle(stream, dev)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(handle, device=dev)
     return torch.cuda.stream(stream), handle
 
 
-def _check_kv8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev):
-    """The paged cache of Hkv heads of D features; returns (n_pages, page_size)."""
+def _cache_checks(k_cache, v_cache, k_scale, v_scale, Hkv, D):
+    """The checks of a paged cache of Hkv heads of D features."""
     import torch
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be (n_pages, Hkv, page_size, D)")
-    n_pages, page_size = k_cache.shape[0], k_cache.shape[2]
-    shape = (n_pages, Hkv, page_size, D)
-    _want("k_cache", k_cache, shape, torch.float8_e4m3fn, dev)
-    _want("v_cache", v_cache, shape, torch.float8_e4m3fn, dev)
-    _want("k_scale", k_scale, (n_pages, Hkv), torch.float32, dev)
-    _want("v_scale", v_scale, (n_pages, Hkv), torch.float32, dev)
-    return n_pages, page_size
+    n_pages, _, page_size, _ = k_cache.shape
+    shape, scales, e4m3, f32 = (n_pages, Hkv, page_size, D), (n_pages, Hkv), torch.float8_e4m3fn, torch.float32
+    return n_pages, page_size, (("k_cache", k_cache, shape, e4m3), ("v_cache", v_cache, shape, e4m3),
+                                ("k_scale", k_scale, scales, f32), ("v_scale", v_scale, scales, f32))
 
 
 def kv_pages(block_table, kv_len, first_page, ring, pool, n_new, page_size: int, window: int = 0, T: int = 1, *,
@@ -646,37 +667,42 @@ def kv_pages(block_table, kv_len, first_page, ring, pool, n_new, page_size: int,
     ``slots`` and ``step_len`` may be passed in (then T is that tensor's)."""
     import torch
     i32 = torch.int32
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be (B, max_pages)")
+    if block_table.dim() != 2 or ring.dim() != 1:
+        raise ValueError("block_table must be (B, max_pages), ring (n_pages,)")
     B, max_pages = block_table.shape
+    n_pages, = ring.shape
     dev = block_table.device
     if out is None:
-        out = (block_table, kv_len, first_page, pool)
-    if len(out) != 4:
-        raise ValueError("out is (block_table, kv_len, first_page, pool)")
-    if ring.dim() != 1:
-        raise ValueError("ring must be (n_pages,)")
-    for name, t, shape in (("block_table", block_table, (B, max_pages)), ("kv_len", kv_len, (B,)),
-                           ("first_page", first_page, (B,)), ("pool", pool, (2,)), ("n_new", n_new, (B,)),
-                           ("ring", ring, ring.shape), ("out[0]", out[0], (B, max_pages)), ("out[1]", out[1], (B,)),
-                           ("out[2]", out[2], (B,)), ("out[3]", out[3], (2,))):
-        _want(name, t, shape, i32, dev)
+        o_table, o_len, o_first, o_pool = block_table, kv_len, first_page, pool
+    else:
+        if len(out) != 4:
+            raise ValueError("out is (block_table, kv_len, first_page, pool)")
+        o_table, o_len, o_first, o_pool = out
     if slots is not None:
         if slots.dim() != 2:
             raise ValueError("slots must be (B, T)")
         T = slots.shape[1]
-        _want("slots", slots, (B, T), i32, dev)
+    table, row, two = (B, max_pages), (B,), (2,)
+    _check_all(dev, (("block_table", block_table, table, i32), ("kv_len", kv_len, row, i32),
+                     ("first_page", first_page, row, i32), ("pool", pool, two, i32), ("n_new", n_new, row, i32),
+                     ("ring", ring, (n_pages,), i32)))
+    if out is not None:
+        _check_all(dev, (("out[0]", o_table, table, i32), ("out[1]", o_len, row, i32), ("out[2]", o_first, row, i32),
+                         ("out[3]", o_pool, two, i32)))
+    if slots is not None:
+        _check_all(dev, (("slots", slots, (B, T), i32),))
     if step_len is not None:
-        _want("step_len", step_len, (B,), i32, dev)
+        _check_all(dev, (("step_len", step_len, row, i32),))
     ctx, st = _on_stream(stream, dev)
     with ctx:
         if slots is None:
-            slots = torch.empty((B, T), dtype=i32, device=dev)
+            slots = torch.empty_strided((B, T), (T, 1), dtype=i32, device=dev)
         if step_len is None:
-            step_len = torch.empty((B,), dtype=i32, device=dev)
-        rc = swa_attn_kv_pages(_ptr(block_table), _ptr(kv_len), _ptr(first_page), _ptr(pool), _ptr(n_new), _ptr(ring),
-                               _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), _ptr(slots), _ptr(step_len),
-                               B, T, max_pages, ring.shape[0], int(page_size), int(window), st)
+            step_len = torch.empty_like(kv_len)
+        rc = _lib.swa_attn_kv_pages(block_table.data_ptr(), kv_len.data_ptr(), first_page.data_ptr(), pool.data_ptr(),
+                                    n_new.data_ptr(), ring.data_ptr(), o_table.data_ptr(), o_len.data_ptr(),
+                                    o_first.data_ptr(), o_pool.data_ptr(), slots.data_ptr(), step_len.data_ptr(), B, T,
+                                    max_pages, n_pages, int(page_size), int(window), st)
     if rc != SWA_OK:
         raise SwaError(rc, "swa_attn_kv_pages")
     return slots, step_len
@@ -689,16 +715,16 @@ def kv8_write(kh, vp, slots, k_cache, v_cache, k_scale, v_scale, *, stream=None)
     import torch
     if kh.dim() != 4:
         raise ValueError("kh and vp must be (B, T, Hkv, D)")
-    B, T, Hkv, D = kh.shape
+    B, T, Hkv, D = shape = kh.shape
     dev = kh.device
-    _want("kh", kh, (B, T, Hkv, D), torch.bfloat16)
-    _want("vp", vp, (B, T, Hkv, D), torch.bfloat16, dev)
-    _want("slots", slots, (B, T), torch.int32, dev)
-    n_pages, page_size = _check_kv8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev)
+    n_pages, page_size, checks = _cache_checks(k_cache, v_cache, k_scale, v_scale, Hkv, D)
+    _check_all(dev, (("kh", kh, shape, torch.bfloat16), ("vp", vp, shape, torch.bfloat16),
+                     ("slots", slots, (B, T), torch.int32), *checks))
     ctx, st = _on_stream(stream, dev)
     with ctx:
-        rc = swa_attn_kv8_write(_ptr(kh), _ptr(vp), _ptr(slots), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                                _ptr(v_scale), B, T, Hkv, D, n_pages, page_size, st)
+        rc = _lib.swa_attn_kv8_write(kh.data_ptr(), vp.data_ptr(), slots.data_ptr(), k_cache.data_ptr(),
+                                     v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, T, Hkv, D, n_pages,
+                                     page_size, st)
     if rc != SWA_OK:
         raise SwaError(rc, "swa_attn_kv8_write")
 
@@ -710,21 +736,23 @@ def kv8_read(slots, k_cache, v_cache, k_scale, v_scale, *, kh=None, vp=None, str
     if slots.dim() != 2 or k_cache.dim() != 4:
         raise ValueError("slots must be (B, T), the caches (n_pages, Hkv, page_size, D)")
     B, T = slots.shape
-    Hkv, D = k_cache.shape[1], k_cache.shape[3]
-    dev = slots.device
-    _want("slots", slots, (B, T), torch.int32)
-    n_pages, page_size = _check_kv8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev)
-    for name, t in (("kh", kh), ("vp", vp)):
-        if t is not None:
-            _want(name, t, (B, T, Hkv, D), torch.bfloat16, dev)
+    _, Hkv, _, D = k_cache.shape
+    dev, bf = slots.device, torch.bfloat16
+    n_pages, page_size, checks = _cache_checks(k_cache, v_cache, k_scale, v_scale, Hkv, D)
+    _check_all(dev, (("slots", slots, (B, T), torch.int32), *checks))
+    if kh is not None:
+        _check_all(dev, (("kh", kh, (B, T, Hkv, D), bf),))
+    if vp is not None:
+        _check_all(dev, (("vp", vp, (B, T, Hkv, D), bf),))
     ctx, st = _on_stream(stream, dev)
     with ctx:
+        strides = (T * Hkv * D, Hkv * D, D, 1)
         if kh is None:
-            kh = torch.empty((B, T, Hkv, D), dtype=torch.bfloat16, device=dev)
+            kh = torch.empty_strided((B, T, Hkv, D), strides, dtype=bf, device=dev)
         if vp is None:
-            vp = torch.empty((B, T, Hkv, D), dtype=torch.bfloat16, device=dev)
-        rc = swa_attn_kv8_read(_ptr(slots), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(kh),
-                               _ptr(vp), B, T, Hkv, D, n_pages, page_size, st)
+            vp = torch.empty_strided((B, T, Hkv, D), strides, dtype=bf, device=dev)
+        rc = _lib.swa_attn_kv8_read(slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                    v_scale.data_ptr(), kh.data_ptr(), vp.data_ptr(), B, T, Hkv, D, n_pages, page_size, st)
     if rc != SWA_OK:
         raise SwaError(rc, "swa_attn_kv8_read")
     return kh, vp
@@ -743,48 +771,44 @@ def decode_kv8(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     import torch
     if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("q must be (B, H, D), the caches (n_pages, Hkv, page_size, D), block_table (B, max_pages)")
-    B, H, D = q.shape
-    Hkv = k_cache.shape[1]
-    dev = q.device
-    bf = torch.bfloat16
-    _want("q", q, (B, H, D), bf)
+    B, H, D = shape = q.shape
+    Hkv, max_pages = k_cache.shape[1], block_table.shape[1]
+    dev, bf, i32 = q.device, torch.bfloat16, torch.int32
     if (k is None) != (v is None):
         raise ValueError("k and v go together")
-    if k is not None:
-        _want("k", k, (B, Hkv, D), bf, dev)
-        _want("v", v, (B, Hkv, D), bf, dev)
     if (ve is None) != (gate_x is None) or (ve is None) != (Wg is None) or (k is None and ve is not None):
         raise ValueError("ve, gate_x and Wg go together, and with k and v")
+    n_pages, page_size, checks = _cache_checks(k_cache, v_cache, k_scale, v_scale, Hkv, D)
+    _check_all(dev, (("q", q, shape, bf), ("block_table", block_table, (B, max_pages), i32),
+                     ("seq_len", seq_len, (B,), i32), *checks))
+    if k is not None:
+        _check_all(dev, (("k", k, (B, Hkv, D), bf), ("v", v, (B, Hkv, D), bf)))
     if ve is not None:
-        _want("ve", ve, (B, Hkv, D), bf, dev)
-        _want("gate_x", gate_x, (B, 32), bf, dev)
-        _want("Wg", Wg, (32, Hkv), bf, dev)
-    n_pages, page_size = _check_kv8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev)
-    max_pages = block_table.shape[1]
-    _want("block_table", block_table, (B, max_pages), torch.int32, dev)
-    _want("seq_len", seq_len, (B,), torch.int32, dev)
+        _check_all(dev, (("ve", ve, (B, Hkv, D), bf), ("gate_x", gate_x, (B, 32), bf), ("Wg", Wg, (32, Hkv), bf)))
     if doc_start is not None:
-        _want("doc_start", doc_start, (B,), torch.int32, dev)
+        _check_all(dev, (("doc_start", doc_start, (B,), i32),))
     if out is not None:
-        _want("out", out, (B, H, D), bf, dev)
+        _check_all(dev, (("out", out, shape, bf),))
     if lse is not None:
-        _want("lse", lse, (B, H), torch.float32, dev)
+        _check_all(dev, (("lse", lse, (B, H), torch.float32),))
     if workspace is not None:
         _want_workspace(workspace, dev)
     ctx, st = _on_stream(stream, dev)
     with ctx:
         if out is None:
-            out = torch.empty((B, H, D), dtype=bf, device=dev)
+            out = torch.empty_like(q)
         if lse is None:
-            lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+            lse = torch.empty_strided((B, H), (H, 1), dtype=torch.float32, device=dev)
         if workspace is None:
-            need = swa_attn_kv8_decode_workspace_bytes(B, H, Hkv, D)
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        rc = swa_attn_kv8_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(ve), _ptr(gate_x), _ptr(Wg), _ptr(k_cache),
-                                 _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_len),
-                                 _ptr(doc_start), _ptr(out), _ptr(lse), B, H, Hkv, D, n_pages, page_size, max_pages,
-                                 int(window), float(rope_base), float(eps), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), st)
+            ws_bytes = _lib.swa_attn_kv8_decode_workspace_bytes(B, H, Hkv, D)
+            workspace = torch.empty_strided((max(ws_bytes, 1),), (1,), dtype=torch.uint8, device=dev)
+        else:
+            ws_bytes = workspace.numel() * workspace.element_size()
+        rc = _lib.swa_attn_kv8_decode(
+            q.data_ptr(), _ptr(k), _ptr(v), _ptr(ve), _ptr(gate_x), _ptr(Wg), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_len.data_ptr(), _ptr(doc_start),
+            out.data_ptr(), lse.data_ptr(), B, H, Hkv, D, n_pages, page_size, max_pages, int(window), float(rope_base),
+            float(eps), workspace.data_ptr(), ws_bytes, st)
     if rc != SWA_OK:
         raise SwaError(rc, "swa_attn_kv8_decode")
     return out, lse

@@ -55,11 +55,21 @@ __device__ __forceinline__ uint32_t max_half(uint32_t m) { return max(m & 0xffff
 
 // Four bf16 (two words) times `inv` -> four e4m3 codes, round to nearest even, clamped at 448.
 __device__ __forceinline__ uint32_t encode4(uint32_t w0, uint32_t w1, float inv) {
-    const float2 a = make_float2(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv);
-    const float2 b = make_float2(__uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv);
+    float2 a = make_float2(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u));
+    float2 b = make_float2(__uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u));
+    a = make_float2(a.x * inv, a.y * inv);
+    b = make_float2(b.x * inv, b.y * inv);
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
+}
+
+__device__ __forceinline__ uint4 ldg_stream16(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
 }
 
 __device__ __forceinline__ float2 decode2(uint32_t two) {
@@ -81,6 +91,8 @@ __device__ __forceinline__ uint32_t recode4(uint32_t c, float down) {
 // slots of one page.  One block per (window of `win` tokens, head) takes the runs that begin in its
 // window: a run of one token by the D/8 lanes of a row group, a longer one by the whole block, its
 // rows kept in registers between the maximum and the encoding, so that khat and v' are read once.
+// HBM-bound on prompts, where most windows are one page: the window's rows are loaded before its slots are
+// known, and used where a run begins with the window.
 struct Kv8Store {
     uint8_t* k_cache;
     uint8_t* v_cache;
@@ -110,9 +122,8 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(const __nv_bfloat16* __r
     const int group = (int)threadIdx.x / TPR, l8 = (int)threadIdx.x % TPR;
     const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
     const int n_slots = c.n_pages << c.log_p;
-    __shared__ int s_run[128], s_n, s_len;
+    __shared__ int s_run[128], s_n, s_len, s_single;
     __shared__ uint32_t s_max[2][8];
-    __shared__ int s_old[2];
 
     auto slot_at = [&](long long t) -> int { return t < n_tokens ? __ldg(slots + t) : -1; };
     // token t goes on where token t - 1 ended
@@ -124,51 +135,40 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(const __nv_bfloat16* __r
         return cache + (((long long)(slot >> c.log_p) * c.Hkv + h) << c.log_p) * D;
     };
 
-    if (threadIdx.x == 0) s_n = 0;
-    __syncthreads();
-    if ((int)threadIdx.x < win) {
-        const long long t = t0 + threadIdx.x;
-        const int s = slot_at(t);
-        if (s >= n_slots) record_error(kErrIndex, kSiteKvSlot);
-        if (s >= 0 && s < n_slots && !goes_on(t) && goes_on(t + 1)) s_run[atomicAdd(&s_n, 1)] = (int)threadIdx.x;
-    }
-    __syncthreads();
-    const int n_runs = s_n;
-    for (int i = 0; i < n_runs; ++i) {
-        const long long t = t0 + s_run[i];
-        if (threadIdx.x == 0) s_len = P;
-        __syncthreads();
-        if (threadIdx.x >= 1 && (int)threadIdx.x < P && !goes_on(t + threadIdx.x)) atomicMin(&s_len, (int)threadIdx.x);
-        const int slot = slot_at(t);
-        const int page = slot >> c.log_p, off = slot & (P - 1);
-        float* sc[2] = {c.k_scale + (long long)page * c.Hkv + h, c.v_scale + (long long)page * c.Hkv + h};
-        if (threadIdx.x < 2) s_old[threadIdx.x] = exponent_of(*sc[threadIdx.x]);
-        __syncthreads();
-        const int len = min(s_len, P - off);
-        uint4 x[2][IT];
-        uint32_t m[2] = {0u, 0u};
+    // the rows of this block's threads from token t on, `len` of them
+    uint4 x[2][IT];
+    auto load_rows = [&](long long t, int len) {
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
             const int r = group + it * RPB;
             if (r < len) {
                 const long long at = ((t + r) * c.Hkv + h) * D + 8 * l8;
-                x[0][it] = *reinterpret_cast<const uint4*>(kh + at);
-                x[1][it] = *reinterpret_cast<const uint4*>(vp + at);
-            } else {
-                x[0][it] = x[1][it] = make_uint4(0u, 0u, 0u, 0u);
+                x[0][it] = ldg_stream16(kh + at);
+                x[1][it] = ldg_stream16(vp + at);
             }
         }
+    };
+    // Rows x of a run of `len` tokens whose first slot is `slot`.
+    auto store_run = [&](int slot, int len) {
+        const int page = slot >> c.log_p, off = slot & (P - 1);
+        float* sc[2] = {c.k_scale + (long long)page * c.Hkv + h, c.v_scale + (long long)page * c.Hkv + h};
+        int old[2] = {kEMin, kEMin};
+        if (off > 0)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) old[u] = exponent_of(*sc[u]);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+            uint32_t m = 0u;
 #pragma unroll
             for (int it = 0; it < IT; ++it)
-                m[u] = max_abs2(max_abs2(max_abs2(max_abs2(m[u], x[u][it].x), x[u][it].y), x[u][it].z), x[u][it].w);
-            uint32_t a = max_half(m[u]);
+                if (group + it * RPB < len)
+                    m = max_abs2(max_abs2(max_abs2(max_abs2(m, x[u][it].x), x[u][it].y), x[u][it].z), x[u][it].w);
+            uint32_t a = max_half(m);
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
             if (lane == 0) s_max[u][warp] = a;
         }
-        __syncthreads();
+        __syncthreads();                   // (and every thread has read the old scales)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             uint32_t a = s_max[u][0];
@@ -177,9 +177,8 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(const __nv_bfloat16* __r
             int e = scale_exponent(a);
             uint8_t* blk = block_of(u == 0 ? c.k_cache : c.v_cache, slot);
             if (off > 0) {
-                const int old = s_old[u];
-                if (e > old) recode_rows<D>(blk, off, scale_of(max(old - e, -126)), group, RPB, l8);
-                e = max(e, old);
+                if (e > old[u]) recode_rows<D>(blk, off, scale_of(max(old[u] - e, -126)), group, RPB, l8);
+                e = max(e, old[u]);
             }
             const float inv = scale_of(-e);
 #pragma unroll
@@ -192,8 +191,47 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(const __nv_bfloat16* __r
             if (threadIdx.x == 0) *sc[u] = scale_of(e);
         }
         __syncthreads();
+    };
+
+    const int here = (int)min((long long)win, n_tokens - t0);      // tokens of the window
+    if (win >= P) load_rows(t0, min(here, P));
+    if (threadIdx.x == 0) {
+        s_n = 0;
+        s_len = P;
+        s_single = 0;
+    }
+    __syncthreads();
+    const int slot0 = slot_at(t0);
+    if ((int)threadIdx.x < win) {
+        const long long t = t0 + threadIdx.x;
+        const int s = slot_at(t);
+        if (s >= n_slots) record_error(kErrIndex, kSiteKvSlot);
+        const bool on = goes_on(t), next_on = goes_on(t + 1);
+        if (s >= 0 && s < n_slots && !on) {
+            if (!next_on) s_single = 1;
+            else if (threadIdx.x > 0 || win < P) s_run[atomicAdd(&s_n, 1)] = (int)threadIdx.x;
+        }
+        if (threadIdx.x > 0 && threadIdx.x < P && !on) atomicMin(&s_len, (int)threadIdx.x);
+    }
+    __syncthreads();
+    // the run that begins with the window: it ends within it, or at the page's end
+    if (win >= P && slot0 >= 0 && slot0 < n_slots && !goes_on(t0)) {
+        const int len = min(s_len, here);
+        if (len > 1) store_run(slot0, len);
+    }
+    const int n_runs = s_n;
+    for (int i = 0; i < n_runs; ++i) {
+        const long long t = t0 + s_run[i];
+        if (threadIdx.x == 0) s_len = P;
+        __syncthreads();
+        if (threadIdx.x >= 1 && (int)threadIdx.x < P && !goes_on(t + threadIdx.x)) atomicMin(&s_len, (int)threadIdx.x);
+        __syncthreads();
+        const int len = s_len;
+        load_rows(t, len);
+        store_run(slot_at(t), len);
     }
     // runs of one token
+    if (s_single == 0) return;
     for (int g0 = 0; g0 < win; g0 += RPB) {
         const long long t = t0 + g0 + group;
         const int slot = g0 + group < win ? slot_at(t) : -1;
@@ -230,36 +268,59 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(const __nv_bfloat16* __r
 
 // -------------------------------------------------------------------------------------------- read
 
-// Row r = token * Hkv + h of the results: D/8 lanes, 8 features each.  Slots below 0 (and past the
-// cache, which is recorded) give zero rows.
+// Row r = token * Hkv + h of the results: D/8 lanes, 8 features each; a thread has kReadRows rows in flight.  Slots
+// below 0 (and past the cache, which is recorded) give zero rows.
+constexpr int kReadRows = 2;
+__device__ __forceinline__ uint2 decode4(uint32_t c, float s) {
+    const float2 a = decode2(c), b = decode2(c >> 16);
+    return make_uint2(pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(b.x * s, b.y * s));
+}
 template <int D>
 __global__ void __launch_bounds__(256) kv8_read_kernel(const int* __restrict__ slots, const Kv8Store c,
                                                        __nv_bfloat16* __restrict__ kh, __nv_bfloat16* __restrict__ vp,
                                                        int n_rows, FastDiv divH) {
-    constexpr int TPR = D / 8;
-    const int l8 = (int)threadIdx.x % TPR;
+    constexpr int TPR = D / 8, STEP = 256 / TPR;
+    const int l8 = 8 * ((int)threadIdx.x % TPR);
     const int n_slots = c.n_pages << c.log_p;
-    for (long long r0 = (blockIdx.x * 256ll + threadIdx.x) / TPR; r0 < n_rows; r0 += gridDim.x * 256ll / TPR) {
-        const int r = (int)r0;
-        const int t = fdiv(r, divH), h = r - t * c.Hkv;
-        const int slot = __ldg(slots + t);
-        uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-        if (slot >= 0 && slot < n_slots) {
-            const long long ph = (long long)(slot >> c.log_p) * c.Hkv + h;
-            const long long at = ((ph << c.log_p) + (slot & ((1 << c.log_p) - 1))) * D + 8 * l8;
+    const long long r0 = (long long)blockIdx.x * STEP * kReadRows + (int)threadIdx.x / TPR;
+    int slot[kReadRows], h[kReadRows];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint2 w = *reinterpret_cast<const uint2*>((u == 0 ? c.k_cache : c.v_cache) + at);
-                const float s = __ldg((u == 0 ? c.k_scale : c.v_scale) + ph);
-                const float2 a = decode2(w.x), b = decode2(w.x >> 16), d = decode2(w.y), e = decode2(w.y >> 16);
-                o[u] = make_uint4(pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(b.x * s, b.y * s),
-                                  pack_bf16x2(d.x * s, d.y * s), pack_bf16x2(e.x * s, e.y * s));
+    for (int x = 0; x < kReadRows; ++x) {
+        const long long r = r0 + x * STEP;
+        slot[x] = -1;
+        if (r < n_rows) {
+            const int t = fdiv((int)r, divH);
+            h[x] = (int)r - t * c.Hkv;
+            slot[x] = __ldg(slots + t);
+            if (slot[x] >= n_slots) {
+                record_error(kErrIndex, kSiteKvSlot);
+                slot[x] = -1;
             }
-        } else if (slot >= n_slots) {
-            record_error(kErrIndex, kSiteKvSlot);
         }
-        *reinterpret_cast<uint4*>(kh + (long long)r * D + 8 * l8) = o[0];
-        *reinterpret_cast<uint4*>(vp + (long long)r * D + 8 * l8) = o[1];
+    }
+    uint2 w[kReadRows][2];
+    float s[kReadRows][2];
+#pragma unroll
+    for (int x = 0; x < kReadRows; ++x) {
+        w[x][0] = w[x][1] = make_uint2(0u, 0u);
+        s[x][0] = s[x][1] = 0.f;
+        if (slot[x] < 0) continue;
+        const long long ph = (long long)(slot[x] >> c.log_p) * c.Hkv + h[x];
+        const long long at = ((ph << c.log_p) + (slot[x] & ((1 << c.log_p) - 1))) * D + l8;
+        w[x][0] = *reinterpret_cast<const uint2*>(c.k_cache + at);
+        w[x][1] = *reinterpret_cast<const uint2*>(c.v_cache + at);
+        s[x][0] = c.k_scale[ph];
+        s[x][1] = c.v_scale[ph];
+    }
+#pragma unroll
+    for (int x = 0; x < kReadRows; ++x) {
+        const long long r = r0 + x * STEP;
+        if (r >= n_rows) continue;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint2 a = decode4(w[x][u].x, s[x][u]), b = decode4(w[x][u].y, s[x][u]);
+            *reinterpret_cast<uint4*>((u == 0 ? kh : vp) + r * D + l8) = make_uint4(a.x, a.y, b.x, b.y);
+        }
     }
 }
 
@@ -301,129 +362,156 @@ struct PageRecord {
     int ring_take, ring_give;   // where in the ring the first taken page is, and the first returned one goes
 };
 
-__device__ __forceinline__ int ring_at(long long i, int n_pages) { return (int)(i % n_pages); }
+constexpr int kPagesSegment = 128;         // entries of a table row, or slots, that a warp has at a time
 
-// Row b of the table and of the slots, by the lanes first, first + step, ...
-__device__ __forceinline__ void pages_fill_row(const PagesParams& p, const PageRecord& r, int b, int first, int step) {
+// One segment of row b: entries of the table (seg < table_segs) or slots.
+__device__ __forceinline__ void pages_fill(const PagesParams& p, const PageRecord& r, int b, int seg, int table_segs,
+                                           int lane) {
     const int* in = p.table + (long long)b * p.max_pages;
-    int* out = p.table_out + (long long)b * p.max_pages;
-    const bool copy = in != out;
-    auto taken = [&](int j) { return p.ring[ring_at((long long)r.ring_take + (j - r.have), p.n_pages)]; };
-    if (copy) {
-        for (int j = first; j < p.max_pages; j += step) {
-            int v = in[j];
+    auto taken = [&](int j) {              // entry j >= have; at most n_pages pages are taken
+        const unsigned x = (unsigned)r.ring_take + (unsigned)(j - r.have);
+        return p.ring[x >= (unsigned)p.n_pages ? x - (unsigned)p.n_pages : x];
+    };
+    if (seg < table_segs) {
+        int* out = p.table_out + (long long)b * p.max_pages;
+        const int first = seg * kPagesSegment;
+        // in place, only what changes is touched
+        if (in == out && first + kPagesSegment <= r.have && (first >= r.upto || first + kPagesSegment <= r.from)) return;
+        if (in == out && first >= r.have + r.take) return;
+        int v[kPagesSegment / 32];
+#pragma unroll
+        for (int x = 0; x < kPagesSegment / 32; ++x) {
+            const int j = first + 32 * x + lane;
+            if (j < p.max_pages) v[x] = j >= r.have && j < r.have + r.take ? taken(j) : in[j];
+        }
+#pragma unroll
+        for (int x = 0; x < kPagesSegment / 32; ++x) {
+            const int j = first + 32 * x + lane;
+            if (j >= p.max_pages) continue;
             if (j >= r.from && j < r.upto) {
-                p.ring[ring_at((long long)r.ring_give + (j - r.from), p.n_pages)] = v;
-                v = -1;
+                p.ring[((unsigned)r.ring_give + (unsigned)(j - r.from)) % (unsigned)p.n_pages] = v[x];
+                v[x] = -1;
             }
-            if (j >= r.have && j < r.have + r.take) v = taken(j);
-            out[j] = v;
+            out[j] = v[x];
         }
-    } else {
-        for (int j = r.from + first; j < r.upto; j += step) {
-            p.ring[ring_at((long long)r.ring_give + (j - r.from), p.n_pages)] = in[j];
-            out[j] = -1;
-        }
-        for (int j = r.have + first; j < r.have + r.take; j += step) out[j] = taken(j);
+        return;
     }
     int* sl = p.slots + (long long)b * p.T;
-    const int P = 1 << p.log_p;
-    for (int t = first; t < p.T; t += step) {
-        int s = -1;
+    const int P = 1 << p.log_p, first = (seg - table_segs) * kPagesSegment;
+    int v[kPagesSegment / 32];
+#pragma unroll
+    for (int x = 0; x < kPagesSegment / 32; ++x) {
+        const int t = first + 32 * x + lane;
+        v[x] = -1;
         if (t < r.n) {
-            const int pos = r.L + t, j = pos >> p.log_p;
-            const int page = j >= r.have ? taken(j) : in[j];
-            if (page >= 0 && page < p.n_pages) s = page * P + (pos & (P - 1));
+            const int j = (r.L + t) >> p.log_p;
+            v[x] = j >= r.have ? taken(j) : in[j];
         }
-        sl[t] = s;
+    }
+#pragma unroll
+    for (int x = 0; x < kPagesSegment / 32; ++x) {
+        const int t = first + 32 * x + lane;
+        if (t < p.T) sl[t] = v[x] >= 0 && v[x] < p.n_pages ? v[x] * P + ((r.L + t) & (P - 1)) : -1;
     }
 }
 
-__global__ void __launch_bounds__(1024) kv_pages_kernel(const PagesParams p) {
+// One cluster: every block goes through all requests (1024 at a time) and finds every record, and the blocks share the
+// rows' segments.  A step in place is safe: a block writes a request's state only after every block has read it, and a row's
+// segments neither read nor write what another one of them changes (the slots read the table entry of a
+// partly filled page, which a step leaves alone; pages are taken from the free stretch of the ring and go back outside it).
+// Latency-bound (the sums, then a table or ring entry, then the stores): one block where all rows are small, else eight.
+__global__ void __launch_bounds__(1024, 1) kv_pages_kernel(const PagesParams p) {
     __shared__ PageRecord s_rec[1024];
-    __shared__ long long s_warp[2][32];
+    __shared__ int s_warp[2][32];
+    __shared__ int s_taken;
     const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+    const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
     const int P = 1 << p.log_p;
     const int head = min(max(p.pool[0], 0), p.n_pages - 1), free = min(max(p.pool[1], 0), p.n_pages);
-    long long base[2] = {0, 0};     // pages wanted and returned by earlier chunks of requests
-    long long taken = 0;
+    const int table_segs = (p.max_pages + kPagesSegment - 1) / kPagesSegment;
+    const int segs = table_segs + (p.T + kPagesSegment - 1) / kPagesSegment;
+    int base[2] = {0, 0};           // pages wanted and returned by earlier chunks of requests (B * max_pages < 2^31)
+    if (threadIdx.x == 0) s_taken = 0;
     for (int b0 = 0; b0 < p.B; b0 += 1024) {
         const int b = b0 + (int)threadIdx.x;
         PageRecord r{};
-        long long need = 0;
-        int F = 0, n = 0, give = 0;
+        int need = 0, F = 0, n = 0, give = 0;
         bool ended = false, fits = false;
         if (b < p.B) {
-            const long long cap = (long long)p.max_pages << p.log_p;
+            const int cap = p.max_pages << p.log_p;
             r.L = p.kv_len[b];
             n = p.n_new[b];
             F = p.first[b];
-            const bool sane = r.L >= 0 && r.L <= cap && F >= 0;
-            if (!sane) r.L = max(0, (int)min((long long)r.L, cap));
-            r.have = (int)(((long long)r.L + P - 1) >> p.log_p);
-            F = min(max(F, 0), r.have);
-            ended = n < 0;
+            // a state that cannot be stays as it is
+            bool sane = r.L >= 0 && r.L <= cap;
+            r.have = sane ? (int)(((unsigned)r.L + P - 1) >> p.log_p) : 0;
+            sane = sane && F >= 0 && F <= r.have;
+            ended = n < 0 && sane;
             const int low = p.W > 0 ? max(0, r.L - p.W + 1) >> p.log_p : 0;
             r.from = F;
-            r.upto = ended ? r.have : max(F, low);
+            r.upto = !sane ? F : ended ? r.have : max(F, low);
             give = r.upto - r.from;
-            fits = sane && n >= 0 && n <= p.T && (long long)r.L + n <= cap;
-            if (fits) need = (((long long)r.L + n + P - 1) >> p.log_p) - r.have;
+            fits = sane && n >= 0 && n <= p.T && n <= cap - r.L;
+            if (fits) need = (int)(((unsigned)(r.L + n) + P - 1) >> p.log_p) - r.have;
         }
         // inclusive sums over the chunk
-        long long v[2] = {need, give};
+        int v[2] = {need, give};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const long long o = __shfl_up_sync(0xffffffffu, v[u], d);
-                if (lane >= d) v[u] += o;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o0 = __shfl_up_sync(0xffffffffu, v[0], d), o1 = __shfl_up_sync(0xffffffffu, v[1], d);
+            if (lane >= d) {
+                v[0] += o0;
+                v[1] += o1;
             }
-            if (lane == 31) s_warp[u][warp] = v[u];
+        }
+        if (lane == 31) {
+            s_warp[0][warp] = v[0];
+            s_warp[1][warp] = v[1];
         }
         __syncthreads();
         if (warp < 2) {
-            long long w = s_warp[warp][lane];
+            int w = s_warp[warp][lane];
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const long long o = __shfl_up_sync(0xffffffffu, w, d);
+                const int o = __shfl_up_sync(0xffffffffu, w, d);
                 if (lane >= d) w += o;
             }
             s_warp[warp][lane] = w;
         }
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < 2; ++u) v[u] += base[u] + (warp > 0 ? s_warp[u][warp - 1] : 0ll);
-        base[0] += s_warp[0][31];
-        base[1] += s_warp[1][31];
+        for (int u = 0; u < 2; ++u) {
+            v[u] += base[u] + (warp > 0 ? s_warp[u][warp - 1] : 0);
+            base[u] += s_warp[u][31];
+        }
         const bool ok = fits && n > 0 && (need == 0 || v[0] <= free);
-        r.take = ok ? (int)need : 0;
+        r.take = ok ? need : 0;
         r.n = ok ? n : 0;
-        r.ring_take = ring_at(head + (v[0] - need), p.n_pages);
-        r.ring_give = ring_at((long long)head + free + (v[1] - give), p.n_pages);
+        r.ring_take = (int)(((unsigned)head + (unsigned)(v[0] - need)) % (unsigned)p.n_pages);
+        r.ring_give = (int)((unsigned)(head + (long long)free) % (unsigned)p.n_pages);
+        r.ring_give = (int)(((unsigned)r.ring_give + (unsigned)(v[1] - give)) % (unsigned)p.n_pages);
         s_rec[threadIdx.x] = r;
-        if (b < p.B) {
+        // the sums only grow: the last served request that takes pages has the largest of theirs
+        const unsigned takers = __ballot_sync(0xffffffffu, r.take > 0);
+        if (takers != 0u && lane == 31 - __clz(takers)) atomicMax(&s_taken, v[0]);
+        if (ranks > 1) cluster_sync_all();
+        else __syncthreads();
+        if (rank == 0 && b < p.B) {
             const int after = ended ? 0 : r.L + r.n;
             p.kv_len_out[b] = after;
             p.first_out[b] = ended ? 0 : r.upto;
             p.step_len[b] = ok ? after : 0;
         }
-        // the last served request that takes pages has the largest sum among them
-        long long mine = r.take > 0 ? v[0] : 0ll;
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, d));
-        __syncthreads();
-        if (lane == 0) s_warp[0][warp] = mine;
-        __syncthreads();
-#pragma unroll 1
-        for (int w = 0; w < 32; ++w) taken = max(taken, s_warp[0][w]);
-        const int n_here = min(1024, p.B - b0);
-        for (int i = warp; i < n_here; i += 32) pages_fill_row(p, s_rec[i], b0 + i, lane, 32);
+        const int work = min(1024, p.B - b0) * segs;
+        for (int x = rank * 32 + warp; x < work; x += ranks * 32) {
+            const int row = x / segs;
+            pages_fill(p, s_rec[row], b0 + row, x - row * segs, table_segs, lane);
+        }
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        p.pool_out[0] = ring_at((long long)head + taken, p.n_pages);
-        p.pool_out[1] = (int)min((long long)p.n_pages, (long long)free - taken + base[1]);
+    if (rank == 0 && threadIdx.x == 0) {
+        p.pool_out[0] = (int)(((unsigned)head + (unsigned)s_taken) % (unsigned)p.n_pages);
+        p.pool_out[1] = (int)min((long long)p.n_pages, (long long)free - s_taken + base[1]);
     }
 }
 

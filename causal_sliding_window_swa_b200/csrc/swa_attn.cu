@@ -1328,7 +1328,23 @@ int swa_attn_kv_pages(const int* block_table, const int* kv_len, const int* firs
     if ((rc = device_ready(&dev)) != SWA_OK) return rc;
     swa::PagesParams p{block_table, kv_len, first_page, pool, n_new, ring, block_table_out, kv_len_out, first_page_out,
                        pool_out, slots, step_len, B, T, max_pages, n_pages, log_p, std::max(0, window)};
-    swa::kv_pages_kernel<<<1, 1024, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    cudaLaunchConfig_t cfg = {};
+    // one block for small steps, a cluster of eight for more table entries and slots
+    const unsigned ranks = (long long)B * ((long long)max_pages + T) <= 4096 ? 1u : 8u;
+    cfg.gridDim = dim3(ranks);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, swa::kv_pages_kernel, p) != cudaSuccess) {
+        cudaGetLastError();
+        return SWA_ERR_CUDA;
+    }
     return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
@@ -1375,7 +1391,8 @@ int swa_attn_kv8_read(const int* slots, const void* k_cache, const void* v_cache
     const swa::Kv8Store c{static_cast<uint8_t*>(const_cast<void*>(k_cache)), static_cast<uint8_t*>(const_cast<void*>(v_cache)),
                           const_cast<float*>(k_scale), const_cast<float*>(v_scale), n_pages, Hkv, log_p};
     const int n_rows = B * T * Hkv;
-    const long long blocks = std::min<long long>(((long long)n_rows * (D / 8) + 255) / 256, 148ll * 64);
+    const int rows_per_block = 256 / (D / 8) * swa::kReadRows;
+    const long long blocks = ((long long)n_rows + rows_per_block - 1) / rows_per_block;
     const swa::FastDiv divH = make_fastdiv(Hkv);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     __nv_bfloat16 *kp = static_cast<__nv_bfloat16*>(kh), *vpp = static_cast<__nv_bfloat16*>(vp);

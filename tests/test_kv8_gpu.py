@@ -104,15 +104,20 @@ def test_allocator_steps_equal_the_plain_ones(B, M, N, P, W, T, steps, in_place)
     swa.check_device_status()
 
 
-def test_allocator_leaves_impossible_requests_alone():
-    state, ring = _state(4, 4, 20)
-    state[1].copy_(i32([-5, 100, 3, 0]))       # no length, more than 4 pages of 16 hold, fine, fine
-    state[2].copy_(i32([0, 0, 0, -1]))
+@pytest.mark.parametrize("T", [1, 2000])
+def test_allocator_leaves_impossible_requests_alone(T):
+    # no length; more than 4 pages of 16 hold; fine; no first page; pages given back that it never had; an ended one of those
+    state, ring = _state(6, 4, 20)
+    state[1].copy_(i32([-5, 100, 3, 0, 20, 65]))
+    state[2].copy_(i32([0, 0, 0, -1, 3, 0]))
     state[0][2, 0] = 19
     state[3].copy_(i32([0, 19]))
-    slots, step_len = swa.kv_pages(state[0], state[1], state[2], ring, state[3], i32([1, 1, 1, 1]), 16)
-    assert step_len.tolist() == [0, 0, 4, 0] and slots.tolist() == [[-1], [-1], [19 * 16 + 3], [-1]]
-    assert state[3].tolist() == [0, 19]
+    was = [t.tolist() for t in state]
+    slots, step_len = swa.kv_pages(state[0], state[1], state[2], ring, state[3], i32([1, 1, 1, 1, 1, -1]), 16, T=T)
+    assert step_len.tolist() == [0, 0, 4, 0, 0, 0]
+    assert slots[:, 0].tolist() == [-1, -1, 19 * 16 + 3, -1, -1, -1] and (slots[:, 1:] == -1).all()
+    was[1][2] = 4
+    assert [t.tolist() for t in state] == was and ring.tolist() == list(range(20))
 
 
 # ---------------------------------------------------------------------------------------- write, read
