@@ -231,7 +231,8 @@ constexpr int kKv8Tiles = kKv8Chunk / 16;
 constexpr int kKv8Sms = 148;
 // Blocks of the attention kernel, at most: two per SM where a warp has one group of eight heads, else one.
 __host__ __device__ constexpr int kv8_max_blocks(int G) { return G <= 8 ? 2 * kKv8Sms : kKv8Sms; }
-constexpr int kKv8MinShare = 4;         // units of a block, where there are few
+constexpr int kKv8ItemCost = 2;         // what an item costs beside its units, in units (sharing out the work)
+constexpr int kKv8MinShare = 6;         // units of a block, where there are few
 constexpr int kKv8StepChunks = 8;       // chunks of a block in the one-launch form, at most
 constexpr int kKv8Whole = 4;            // items of at most so many units are not split
 constexpr float kSlack = 10.f;          // fp16 holds 2^15
@@ -253,8 +254,8 @@ struct Kv8AttnParams {
     unsigned long long wait_limit_ns;
 };
 
-// NT groups of eight query heads per warp; NRG sets of warps that split more groups than that.
-template <int D, int NT, int NRG>
+// NT groups of eight query heads per warp; NRG sets of warps that split more groups than that; NSTAGES ring stages.
+template <int D, int NT, int NRG, int NSTAGES>
 struct Kv8Cfg {
     static constexpr int CONSUMERS = 8;
     static constexpr int THREADS = 32 * (CONSUMERS + 1);
@@ -263,24 +264,27 @@ struct Kv8Cfg {
     static constexpr int SETS = KSLOTS / kKv8Tiles;              // chunks in work at a time
     static constexpr int TENSOR = kKv8Chunk * D;                 // bytes of a chunk's K (and V)
     static constexpr int HEADS = 8 * NT;                         // query heads of a warp
-    // results of half of the warps (the other half's are added in registers first); later 4 KB of sums and the
-    // factors of an item's pieces
-    static constexpr int MERGE0 = CONSUMERS / 2 * HEADS * D * 4;
-    static constexpr int MERGE1 = 4096 + kKv8Sms * BLOCKS_PER_SM * HEADS * NRG * 4;
-    static constexpr int MERGE = MERGE0 > MERGE1 ? MERGE0 : MERGE1;
-    // Ring stages; a multiple of SETS, so that a set of warps takes every use of its stages and its waits see each
+    static constexpr int NTG = NT * NRG;                         // groups of eight heads
+    // Ring stages: a multiple of SETS, so that a set of warps takes every use of its stages and its waits see each
     // phase of their barriers in turn.
-    static constexpr int NS = NT == 1 ? (D == 128 ? 4 : 10) : (D == 128 ? 8 : 12);
+    static constexpr int NS = NSTAGES;
+    // one head in two of half of the warps' results
+    static constexpr int MERGE = CONSUMERS / 2 * (HEADS / 2) * D * 4;
     static constexpr int OFF_O = NS * 2 * TENSOR;
     static constexpr int OFF_ML = OFF_O + MERGE;                 // m [8][HEADS], l [8][HEADS]
-    static constexpr int NTG = NT * NRG;                         // groups of eight heads
     static constexpr int OFF_Q = OFF_ML + 2 * CONSUMERS * HEADS * 4;      // qhat as fp16 operands
     static constexpr int OFF_META = OFF_Q + NTG * 8 * D * 2;     // per stage and tile: ks c1, vs, log2 vs, pad
     static constexpr int OFF_BAR = OFF_META + NS * kKv8Tiles * 16;
     static constexpr int SMEM = OFF_BAR + 2 * NS * 8 + 1024;     // + alignment slack
     static_assert(NS % SETS == 0, "a stage belongs to one set of warps");
+    static_assert(MERGE >= 4096, "the sums of a shared item's pieces");
     static_assert(BLOCKS_PER_SM * (SMEM + 2048) <= 228 * 1024, "shared memory");
 };
+// The attention kernel's and, with room for its own tables, the one-launch form's.
+template <int D, int NT, int NRG>
+using Kv8AttnCfg = Kv8Cfg<D, NT, NRG, D == 128 ? (NT == 1 ? 6 : 8) : 12>;
+template <int D>
+using Kv8StepCfg = Kv8Cfg<D, 1, 1, D == 128 ? 4 : 8>;
 
 // First visible key of a request of n tokens.
 __device__ __forceinline__ int kv8_first_key(const Kv8AttnParams& p, int b, int n) {
@@ -294,7 +298,9 @@ struct Kv8Walk {
     int b, hk;             // item
     int n, lo;             // its visible keys [lo, n)
     int ch0, nch;          // its chunks [ch0, ch0 + nch)
-    int begin;             // its first unit
+    int begin;             // its first unit; it has size() of them, of which the last kKv8ItemCost stand for its cost
+
+    __device__ __forceinline__ int size() const { return nch + kKv8ItemCost; }
 
     __device__ __forceinline__ void load(const Kv8AttnParams& p) {
         n = kv8_length(p.seq_len, b, p.max_pages, p.c.log_p);
@@ -304,7 +310,7 @@ struct Kv8Walk {
     }
     // to the item after this one
     __device__ __forceinline__ void next(const Kv8AttnParams& p) {
-        begin += nch;
+        begin += size();
         if (++hk < p.c.Hkv) return;
         hk = 0;
         do {
@@ -545,6 +551,7 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
         }
         u += f.chunks;
         c += f.chunks;
+        if (u == w.begin + w.nch) u = w.begin + w.size();
         if (c == c_end && u < u1) {
             w.next(p);
             c = w.ch0;
@@ -669,35 +676,36 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
         for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], d);
-    // place `at` of the buffer; heads past the group are left out
-    auto put = [&](int at) {
+    // The heads of one parity at a time, for the buffer's sake: half of the warps put theirs down, the others add them to
+    // their own and put those down.
+    constexpr int HH = C::HEADS / 2, KH = C::KSLOTS / 2;
+    const bool upper = warp >= C::CONSUMERS / 2;
+    const int place = (upper ? warp - C::CONSUMERS / 2 : warp) * HH;
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
+    for (int e = 0; e < 2; ++e) {
+        if (e == 1 && p.G == 1) break;
+        auto put = [&]() {                 // heads past the group are left out
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int hc = 8 * x + 2 * t + e;
-                if (h_base + hc >= p.G) continue;
+            for (int x = 0; x < NT; ++x) {
+                if (h_base + 8 * x + 2 * t + e >= p.G) continue;
+                const int at = place + 4 * x + t;
                 if (g == 0) {
-                    sh.m[at * C::HEADS + hc] = m[x][e];
-                    sh.l[at * C::HEADS + hc] = l[x][e];
+                    sh.m[at] = m[x][e];
+                    sh.l[at] = l[x][e];
                 }
 #pragma unroll
                 for (int k = 0; k < 2 * VW; ++k)
-                    *reinterpret_cast<float2*>(sh.o + (at * C::HEADS + hc) * D + 4 * VW * g + 2 * k) =
-                        make_float2(o[x][k][e], o[x][k][2 + e]);
+                    *reinterpret_cast<float2*>(sh.o + at * D + 4 * VW * g + 2 * k) = make_float2(o[x][k][e], o[x][k][2 + e]);
             }
-    };
-    const bool upper = warp >= C::CONSUMERS / 2;
-    if (upper) put(warp - C::CONSUMERS / 2);
-    kv8_consumers_sync();
-    if (!upper) {
+        };
+        if (e == 1) kv8_consumers_sync();  // the other parity has been read
+        if (upper) put();
+        kv8_consumers_sync();
+        if (!upper) {
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int hc = 8 * x + 2 * t + e;
-                if (h_base + hc >= p.G) continue;
-                const int at = warp * C::HEADS + hc;
+            for (int x = 0; x < NT; ++x) {
+                if (h_base + 8 * x + 2 * t + e >= p.G) continue;
+                const int at = place + 4 * x + t;
                 const float m2 = sh.m[at], l2 = sh.l[at];
                 const float M = fmaxf(m[x][e], m2);
                 const float f1 = kv8_factor(m[x][e], l[x][e], M), f2 = kv8_factor(m2, l2, M);
@@ -710,31 +718,32 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
                 m[x][e] = M;
                 l[x][e] = l[x][e] * f1 + l2 * f2;
             }
-    }
-    __syncwarp();
-    if (!upper) put(warp);                 // where it has just read
-    kv8_consumers_sync();
-    for (int x = (int)threadIdx.x; x < p.G * (D / 4); x += 256) {
-        const int h = x / (D / 4), d4 = x % (D / 4);
-        const int r = h / C::HEADS, hc = h % C::HEADS;
-        constexpr int KH = C::KSLOTS / 2;
-        float M = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < KH; ++k) M = fmaxf(M, sh.m[(k * NRG + r) * C::HEADS + hc]);
-        float L = 0.f;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < KH; ++k) {
-            const int at = (k * NRG + r) * C::HEADS + hc;
-            const float f = kv8_factor(sh.m[at], sh.l[at], M);
-            const float4 v = *reinterpret_cast<const float4*>(sh.o + at * D + 4 * d4);
-            L = fmaf(sh.l[at], f, L);
-            O.x = fmaf(v.x, f, O.x);
-            O.y = fmaf(v.y, f, O.y);
-            O.z = fmaf(v.z, f, O.z);
-            O.w = fmaf(v.w, f, O.w);
+            __syncwarp();
+            put();                         // where it has just read
         }
-        emit(h, d4, O, M, L);
+        kv8_consumers_sync();
+        const int n_heads = (p.G + 1 - e) / 2;                  // heads 2 y + e
+        for (int x = (int)threadIdx.x; x < n_heads * (D / 4); x += 256) {
+            const int y = x / (D / 4), d4 = x % (D / 4);
+            const int r = y / HH, yc = y % HH;
+            float M = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < KH; ++k) M = fmaxf(M, sh.m[(k * NRG + r) * HH + yc]);
+            float L = 0.f;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < KH; ++k) {
+                const int at = (k * NRG + r) * HH + yc;
+                const float f = kv8_factor(sh.m[at], sh.l[at], M);
+                const float4 v = *reinterpret_cast<const float4*>(sh.o + at * D + 4 * d4);
+                L = fmaf(sh.l[at], f, L);
+                O.x = fmaf(v.x, f, O.x);
+                O.y = fmaf(v.y, f, O.y);
+                O.z = fmaf(v.z, f, O.z);
+                O.w = fmaf(v.w, f, O.w);
+            }
+            emit(2 * y + e, d4, O, M, L);
+        }
     }
 }
 
@@ -753,10 +762,10 @@ __device__ __forceinline__ uint2 bf16x4_to_half4(uint2 raw) {
 
 // tm_k, tm_v: the caches as {D, n_pages * Hkv * P} bytes.
 template <int D, int NT, int NRG>
-__global__ void __launch_bounds__(Kv8Cfg<D, NT, NRG>::THREADS, Kv8Cfg<D, NT, NRG>::BLOCKS_PER_SM)
+__global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D, NT, NRG>::BLOCKS_PER_SM)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const Kv8AttnParams p) {
-    using C = Kv8Cfg<D, NT, NRG>;
+    using C = Kv8AttnCfg<D, NT, NRG>;
     extern __shared__ __align__(1024) uint8_t dsmem[];
     const Kv8Shared<C> sh(dsmem);
     __shared__ int s_warp_sum[C::CONSUMERS + 1];
@@ -775,7 +784,7 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NT, NRG>::THREADS, Kv8Cfg<D, NT, NRG
     int mine = 0;
     for (w.b = b_lo; w.b < b_hi; ++w.b) {
         w.load(p);
-        mine += w.nch;
+        if (w.nch > 0) mine += w.size();
     }
     int incl = mine;
 #pragma unroll
@@ -795,7 +804,8 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NT, NRG>::THREADS, Kv8Cfg<D, NT, NRG
     const int n_blocks = min((int)gridDim.x, (n_units + kKv8MinShare - 1) / kKv8MinShare);
     if ((int)blockIdx.x >= n_blocks) return;
     const Kv8Shares shares(n_units, n_blocks);
-    // Where this block's stretch begins and ends: a boundary inside a small item moves to that item's end.
+    // Where this block's stretch begins and ends: a boundary inside a small item, or among the units of an item's
+    // cost, moves to that item's end.
     const int r0 = shares.begin(blockIdx.x), r1 = shares.begin(blockIdx.x + 1);
     if (blockIdx.x + 1 == n_blocks && threadIdx.x == 0) s_to = n_units;
 #pragma unroll
@@ -805,11 +815,12 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NT, NRG>::THREADS, Kv8Cfg<D, NT, NRG
         int before = incl - mine;
         for (w.b = b_lo;; ++w.b) {
             w.load(p);
-            if (r < (before + w.nch) * p.c.Hkv) break;
-            before += w.nch;
+            if (w.nch == 0) continue;
+            if (r < (before + w.size()) * p.c.Hkv) break;
+            before += w.size();
         }
-        const int hk = (r - before * p.c.Hkv) / w.nch, begin = before * p.c.Hkv + hk * w.nch;
-        const int at = r > begin && w.nch <= kKv8Whole ? begin + w.nch : r;
+        const int hk = (r - before * p.c.Hkv) / w.size(), begin = before * p.c.Hkv + hk * w.size();
+        const int at = r > begin && (w.nch <= kKv8Whole || r >= begin + w.nch) ? begin + w.size() : r;
         if (side == 0) {
             s_from[0] = w.b;
             s_from[1] = hk;
@@ -826,7 +837,7 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NT, NRG>::THREADS, Kv8Cfg<D, NT, NRG
     w.hk = s_from[1];
     w.begin = s_from[2];
     w.load(p);
-    if (u0 == w.begin + w.nch) w.next(p);
+    if (u0 == w.begin + w.size()) w.next(p);
 
     if (warp == C::CONSUMERS) {
         kv8_produce<D, C, false>(tm_k, tm_v, p, sh, w, u0, u1, lane, false);
@@ -836,7 +847,7 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NT, NRG>::THREADS, Kv8Cfg<D, NT, NRG
     bool ok = true;
     int i = 0;
     for (int u = u0; u < u1;) {
-        const int end = min(u1, w.begin + w.nch);
+        const int end = min(u1, w.begin + w.nch);      // of its units with keys
         for (int x = (int)threadIdx.x; x < C::NTG * 8 * (D / 4); x += 256) {
             const int h = x / (D / 4), f = 4 * (x % (D / 4));
             uint2 raw = make_uint2(0u, 0u);
@@ -860,74 +871,89 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NT, NRG>::THREADS, Kv8Cfg<D, NT, NRG
         if (!alone) {
             const int c_first = shares.owner(w.begin);
             const int pieces = shares.owner(w.begin + w.nch - 1) - c_first + 1;
-            __threadfence();
             kv8_consumers_sync();
-            if (threadIdx.x == 0) s_last = atomicAdd(p.counters + c_first, 1) == pieces - 1;
+            if (threadIdx.x == 0) {        // releases the block's piece, and takes in the others'
+                __threadfence();
+                s_last = atomicAdd(p.counters + c_first, 1) == pieces - 1;
+                __threadfence();
+            }
             kv8_consumers_sync();
             if (s_last) {
-                __threadfence();
                 const int first_slot = 2 * c_first + (shares.begin(c_first) < w.begin ? 1 : 0);
                 auto part = [&](int k, int h) {
                     return p.part + ((long long)(k == 0 ? first_slot : 2 * (c_first + k)) * p.G + h) * (D + 4);
                 };
-                // each head's reference and sum, and every piece's factor: a warp per head, a lane per piece
+                // four features to a thread; with few heads, several threads share the pieces, four loads at a time
                 float4* s_sum = reinterpret_cast<float4*>(sh.o);
-                float* s_f = sh.o + 1024;
-                for (int h = warp; h < p.G; h += C::CONSUMERS) {
-                    float M = -INFINITY, L = 0.f;
-                    for (int k = lane; k < pieces; k += 32) M = fmaxf(M, __ldcg(part(k, h) + D));
-#pragma unroll
-                    for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-                    for (int k = lane; k < pieces; k += 32) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(k, h) + D));
-                        const float f = kv8_factor(ml.x, ml.y, M);
-                        s_f[k * p.G + h] = f;
-                        L = fmaf(ml.y, f, L);
-                    }
-#pragma unroll
-                    for (int d = 16; d >= 1; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-                    if (lane == 0) {
-                        sh.m[h] = M;
-                        sh.l[h] = L;
-                    }
-                }
-                kv8_consumers_sync();
-                // four features to a thread; with few heads, several threads share the pieces
                 const int n_out = p.G * (D / 4), share = n_out < 256 ? 256 / n_out : 1;
                 for (int x = (int)threadIdx.x; x < n_out * share; x += 256) {
                     const int ox = x % n_out, h = ox / (D / 4), d4 = ox % (D / 4);
+                    float M = -INFINITY, L = 0.f;
                     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int k = x / n_out; k < pieces; k += share) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part(k, h)) + d4);
-                        const float f = s_f[k * p.G + h];
-                        O.x = fmaf(v.x, f, O.x);
-                        O.y = fmaf(v.y, f, O.y);
-                        O.z = fmaf(v.z, f, O.z);
-                        O.w = fmaf(v.w, f, O.w);
+                    for (int k0 = x / n_out; k0 < pieces; k0 += 4 * share) {
+                        float4 v[4];
+                        float2 ml[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int k = k0 + y * share;
+                            v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            ml[y] = make_float2(-INFINITY, 0.f);
+                            if (k < pieces) {
+                                v[y] = __ldcg(reinterpret_cast<const float4*>(part(k, h)) + d4);
+                                ml[y] = __ldcg(reinterpret_cast<const float2*>(part(k, h) + D));
+                            }
+                        }
+                        const float M2 = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+                        const float f0 = kv8_factor(M, L, M2);
+                        L *= f0;
+                        O.x *= f0;
+                        O.y *= f0;
+                        O.z *= f0;
+                        O.w *= f0;
+                        M = M2;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float f = kv8_factor(ml[y].x, ml[y].y, M);
+                            L = fmaf(ml[y].y, f, L);
+                            O.x = fmaf(v[y].x, f, O.x);
+                            O.y = fmaf(v[y].y, f, O.y);
+                            O.z = fmaf(v[y].z, f, O.z);
+                            O.w = fmaf(v[y].w, f, O.w);
+                        }
                     }
-                    if (share > 1) s_sum[x] = O;
-                    else kv8_store4<D>(p, w.b, w.hk, h, d4, O, sh.m[h], sh.l[h]);
+                    if (share == 1) {
+                        kv8_store4<D>(p, w.b, w.hk, h, d4, O, M, L);
+                    } else {
+                        s_sum[x] = O;
+                        if (d4 == 0) {     // of (share, head)
+                            sh.m[x / (D / 4)] = M;
+                            sh.l[x / (D / 4)] = L;
+                        }
+                    }
                 }
                 if (share > 1) {
                     kv8_consumers_sync();
                     if ((int)threadIdx.x < n_out) {
                         const int h = (int)threadIdx.x / (D / 4), d4 = (int)threadIdx.x % (D / 4);
-                        float4 O = s_sum[threadIdx.x];
-                        for (int k = 1; k < share; ++k) {
+                        float M = -INFINITY, L = 0.f;
+                        for (int k = 0; k < share; ++k) M = fmaxf(M, sh.m[k * p.G + h]);
+                        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int k = 0; k < share; ++k) {
+                            const float f = kv8_factor(sh.m[k * p.G + h], sh.l[k * p.G + h], M);
                             const float4 v = s_sum[k * n_out + threadIdx.x];
-                            O.x += v.x;
-                            O.y += v.y;
-                            O.z += v.z;
-                            O.w += v.w;
+                            L = fmaf(sh.l[k * p.G + h], f, L);
+                            O.x = fmaf(v.x, f, O.x);
+                            O.y = fmaf(v.y, f, O.y);
+                            O.z = fmaf(v.z, f, O.z);
+                            O.w = fmaf(v.w, f, O.w);
                         }
-                        kv8_store4<D>(p, w.b, w.hk, h, d4, O, sh.m[h], sh.l[h]);
+                        kv8_store4<D>(p, w.b, w.hk, h, d4, O, M, L);
                     }
                 }
                 kv8_consumers_sync();      // before the buffer is written again
             }
         }
-        u = end;
+        u = end == w.begin + w.nch ? w.begin + w.size() : end;
         if (u < u1) w.next(p);
     }
 }
@@ -939,10 +965,10 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NT, NRG>::THREADS, Kv8Cfg<D, NT, NRG
 // Against the two kernels: no dependent launch and nothing in global memory between the blocks (a d24 request of
 // 301 tokens 9 -> 7 us), but the split follows each item alone, so the GPU is not shared evenly by many ragged ones.
 template <int D>
-__global__ void __launch_bounds__(Kv8Cfg<D, 1, 1>::THREADS, 2)
+__global__ void __launch_bounds__(Kv8StepCfg<D>::THREADS, 2)
     kv8_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Kv8AttnParams p,
                     const Kv8TokenParams tk) {
-    using C = Kv8Cfg<D, 1, 1>;
+    using C = Kv8StepCfg<D>;
     constexpr int TPR = D / 8, HALF = D / 2;
     extern __shared__ __align__(1024) uint8_t dsmem[];
     const Kv8Shared<C> sh(dsmem);

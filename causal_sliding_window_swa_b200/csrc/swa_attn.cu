@@ -1444,7 +1444,7 @@ bool make_page_map(CUtensorMap* m, const void* base, long long rows, int D, int 
 template <int D, int NT, int NRG>
 int launch_kv8_attention_n(int dev, const CUtensorMap& tk, const CUtensorMap& tv, const swa::Kv8AttnParams& a,
                            cudaStream_t st) {
-    using C = swa::Kv8Cfg<D, NT, NRG>;
+    using C = swa::Kv8AttnCfg<D, NT, NRG>;
     static std::once_flag once[64];
     static bool ok[64] = {false};
     std::call_once(once[dev], [&] {
@@ -1464,7 +1464,7 @@ int launch_kv8_attention_n(int dev, const CUtensorMap& tk, const CUtensorMap& tv
 template <int D>
 int launch_kv8_step(int dev, const CUtensorMap& tk, const CUtensorMap& tv, const swa::Kv8AttnParams& a,
                     const swa::Kv8TokenParams& t, int ranks, cudaStream_t st) {
-    using C = swa::Kv8Cfg<D, 1, 1>;
+    using C = swa::Kv8StepCfg<D>;
     static std::once_flag once[64];
     static bool ok[64] = {false};
     std::call_once(once[dev], [&] {
@@ -1545,7 +1545,7 @@ int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void*
     if (!block_table || !seq_len || !workspace || max_pages < 1) return SWA_ERR_INVALID_ARG;
     // positions and the attention's units (64 positions of a request and head) within int32
     if ((long long)max_pages * page_size >= (1ll << 31) ||
-        ((long long)max_pages * page_size / swa::kKv8Chunk + 1) * B * Hkv >= (1ll << 31))
+        ((long long)max_pages * page_size / swa::kKv8Chunk + 1 + swa::kKv8ItemCost) * B * Hkv >= (1ll << 31))
         return SWA_ERR_UNSUPPORTED;
     if (!aligned(block_table, 4) || !aligned(seq_len, 4) || (doc_start && !aligned(doc_start, 4)) || !aligned(workspace, 16))
         return SWA_ERR_MISALIGNED;
