@@ -330,10 +330,12 @@ struct Kv8Shares {
     }
 };
 
-__device__ __forceinline__ uint32_t fp8x2_to_half2(uint32_t two) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two));
-    return r;
+// Four e4m3 codes -> two pairs of fp16, exact.
+__device__ __forceinline__ void fp8x4_to_half4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -391,8 +393,9 @@ __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0
         if ((st & 1) == 0)
 #pragma unroll
             for (int x = 0; x < NT; ++x) qs[x] = q[(x * (NSTEP / 2) + st / 2) * 32];
-        const uint32_t a0 = fp8x2_to_half2(a[0][st]), a1 = fp8x2_to_half2(a[1][st]);
-        const uint32_t a2 = fp8x2_to_half2(a[0][st] >> 16), a3 = fp8x2_to_half2(a[1][st] >> 16);
+        uint32_t a0, a1, a2, a3;
+        fp8x4_to_half4(a[0][st], a0, a2);
+        fp8x4_to_half4(a[1][st], a1, a3);
 #pragma unroll
         for (int x = 0; x < NT; ++x)
             mma_16816(sc[x][st % NC], a0, a1, a2, a3, (st & 1) ? qs[x].z : qs[x].x, (st & 1) ? qs[x].w : qs[x].y);
@@ -465,10 +468,11 @@ __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0
 #pragma unroll
     for (int k = 0; k < VW; ++k) {
         // features 4 k .. 4 k + 3 of this lane, keys (2 t, 2 t + 1) and (2 t + 8, 2 t + 9)
-        const uint32_t p0 = __byte_perm(v[0][k], v[1][k], 0x5140), p1 = __byte_perm(v[2][k], v[3][k], 0x5140);
-        const uint32_t r0 = __byte_perm(v[0][k], v[1][k], 0x7362), r1 = __byte_perm(v[2][k], v[3][k], 0x7362);
-        const uint32_t a0 = fp8x2_to_half2(p0), a1 = fp8x2_to_half2(p0 >> 16), a2 = fp8x2_to_half2(p1), a3 = fp8x2_to_half2(p1 >> 16);
-        const uint32_t c0 = fp8x2_to_half2(r0), c1 = fp8x2_to_half2(r0 >> 16), c2 = fp8x2_to_half2(r1), c3 = fp8x2_to_half2(r1 >> 16);
+        uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
+        fp8x4_to_half4(__byte_perm(v[0][k], v[1][k], 0x5140), a0, a1);
+        fp8x4_to_half4(__byte_perm(v[2][k], v[3][k], 0x5140), a2, a3);
+        fp8x4_to_half4(__byte_perm(v[0][k], v[1][k], 0x7362), c0, c1);
+        fp8x4_to_half4(__byte_perm(v[2][k], v[3][k], 0x7362), c2, c3);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             mma_16816(o[x][2 * k], a0, a1, a2, a3, b[x][0], b[x][1]);
@@ -530,16 +534,20 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
                                             const Kv8Shared<C>& sh, Kv8Walk w, int u0, int u1, int lane, bool append) {
     // A box is a page, or the half of a 128-token page that a chunk has.
     const int box_log = min(p.c.log_p, 6), nb_log = 6 - box_log;   // 64 >> nb_log keys; boxes of a chunk
-    const int tiles = (1 << box_log) / 16;
     const uint32_t box_bytes = (uint32_t)((1 << box_log) * D);
-    // A batch: the boxes, one to a lane, of up to 32 >> nb_log chunks of an item.
-    struct Batch {
+    // A batch: the boxes, one to a lane, of up to 32 >> nb_log chunks of an item.  Its table entries are loaded two
+    // batches ahead, its scales one: one warp feeds the block, and what it spends on a chunk bounds the block's rate.
+    struct Pages {
         int chunks, hk, page, sub;     // this lane's table entry (kNone: not wanted), its first row in the page
+    };
+    struct Boxes {
+        int chunks, ph, row;           // this lane's page and head, and its first row in the cache (-1: none)
+        float ks, vs;
     };
     constexpr int kNone = INT_MIN;
     int u = u0, c = w.ch0 + (u0 - w.begin);
     auto look_up = [&]() {
-        Batch f{0, w.hk, kNone, 0};
+        Pages f{0, w.hk, kNone, 0};
         if (u >= u1) return f;
         const int c_end = w.ch0 + (min(u1, w.begin + w.nch) - w.begin);
         f.chunks = min(32 >> nb_log, c_end - c);
@@ -558,86 +566,114 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
         }
         return f;
     };
-    bool ok = true;
-    int i = 0;                                                 // chunks before this batch
-    Batch f = look_up();
+    auto load_scales = [&](Boxes& x) {
+        if (x.row >= 0) {              // volatile: the token may be written while this block runs
+            x.ks = *(const volatile float*)(p.c.k_scale + x.ph);
+            x.vs = *(const volatile float*)(p.c.v_scale + x.ph);
+        }
+    };
+    auto find = [&](const Pages& f) {
+        Boxes x{f.chunks, 0, -1, 0.f, -1.f};
+        if (f.page >= 0 && f.page < p.c.n_pages) {
+            x.ph = f.page * p.c.Hkv + f.hk;
+            x.row = (x.ph << p.c.log_p) + f.sub;
+            load_scales(x);
+        } else if (f.page != kNone) {
+            record_error(kErrIndex, kSiteKvPage);
+        }
+        return x;
+    };
+    int s = 0, uses = 0;               // the next stage, and how often the ring has gone round
+    // Chunk k's copies into stage `st`; its scales.
+    auto copy = [&](const Boxes& x, int k, int st, bool with_scales, const float4& meta) {
+        const int rel = lane - (k << nb_log);
+        const bool here = (unsigned)rel < (1u << nb_log), load = here && x.row >= 0;
+        if (with_scales && here) sh.meta[st * kKv8Tiles + rel] = meta;
+        const uint32_t n_load = (uint32_t)__popc(__ballot_sync(0xffffffffu, load));
+        const uint32_t bar = smem_u32(sh.full + st);
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, n_load * 2u * box_bytes);
+            if (with_scales) mbar_arrive(bar);
+        }
+        __syncwarp();
+        if (load) {
+            const uint32_t dst = smem_u32(sh.ring) + (uint32_t)(2 * st) * C::TENSOR + (uint32_t)rel * box_bytes;
+            tma_load_2d(dst, &tm_k, bar, 0, x.row);
+            tma_load_2d(dst + C::TENSOR, &tm_v, bar, 0, x.row);
+        }
+    };
+    auto meta_of = [&](const Boxes& x) { return make_float4(x.ks * p.c1, x.row >= 0 ? x.vs : -1.f, log2f(x.vs), 0.f); };
+
+    Pages f = look_up();
     if (!kAppend) {
         // the new tokens' codes and scales
         grid_dependency_wait();
         asm volatile("fence.proxy.async.global;" ::: "memory");
     }
-    while (f.chunks > 0 && ok) {
-        const Batch after = look_up();
-        const int ph = f.page * p.c.Hkv + f.hk;
-        const bool there = f.page >= 0 && f.page < p.c.n_pages;
-        if (!there && f.page != kNone) record_error(kErrIndex, kSiteKvPage);
-        const int row = there ? (ph << p.c.log_p) + f.sub : -1;
-        // The copies run ahead of the scales, by at most the ring; a stage is full when it has both.
-        int copied = 0, told = 0;
-        auto copy = [&]() {
-            const int s = (i + copied) % C::NS, rel = lane - (copied << nb_log);   // this lane's box within the chunk
-            const bool load = rel >= 0 && rel < (1 << nb_log) && row >= 0;
-            const uint32_t n_load = (uint32_t)__popc(__ballot_sync(0xffffffffu, load));
-            const uint32_t bar = smem_u32(sh.full + s);
-            if (lane == 0) mbar_arrive_expect_tx(bar, n_load * 2u * box_bytes);
+    Boxes x = find(f);
+    f = look_up();
+    // the first copies do not wait for the scales
+    const bool hold = kAppend && append;                       // the last chunk waits for the block's own token
+    int ahead = min(x.chunks - (hold && f.chunks == 0 ? 1 : 0), C::NS);
+    for (int k = 0; k < ahead; ++k) copy(x, k, k, false, make_float4(0.f, 0.f, 0.f, 0.f));
+    bool ok = true;
+    while (x.chunks > 0 && ok) {
+        float4 meta = meta_of(x);
+        for (int k = 0; k < ahead; ++k) {
+            const int rel = lane - (k << nb_log);
+            if ((unsigned)rel < (1u << nb_log)) sh.meta[k * kKv8Tiles + rel] = meta;
             __syncwarp();
-            if (load) {
-                const uint32_t dst = smem_u32(sh.ring) + (uint32_t)(2 * s) * C::TENSOR + (uint32_t)rel * box_bytes;
-                tma_load_2d(dst, &tm_k, bar, 0, row);
-                tma_load_2d(dst + C::TENSOR, &tm_v, bar, 0, row);
+            if (lane == 0) mbar_arrive(smem_u32(sh.full + k));
+            if (++s == C::NS) {
+                s = 0;
+                ++uses;
             }
-            ++copied;
-        };
-        if (kAppend && append && after.chunks == 0) {
-            while (copied < f.chunks - 1 && i + copied < C::NS) copy();
-            asm volatile("bar.sync 2, %0;" ::"n"(C::THREADS) : "memory");
-            asm volatile("fence.proxy.async.global;" ::: "memory");
         }
-        float ks = 0.f, vs = 0.f;
-        if (there) {
-            ks = *(const volatile float*)(p.c.k_scale + ph);
-            vs = *(const volatile float*)(p.c.v_scale + ph);
-        }
-        while (told < f.chunks) {
-            while (copied < f.chunks && copied < told + C::NS) {
-                const int k = i + copied;
-                if (k >= C::NS) {
-                    const uint32_t bar = smem_u32(sh.empty + k % C::NS), parity = (uint32_t)((k / C::NS) - 1) & 1u;
-                    if (copied > told) {                       // scales wait to be passed on: do not wait here
-                        if (!__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) break;
-                    } else if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_limit_ns, kSiteKv8Empty))) {
-                        ok = false;
-                        break;
-                    }
-                }
-                copy();
+        const bool last = f.chunks == 0;
+        const Boxes y = find(f);
+        f = look_up();
+        for (int k = ahead; k < x.chunks; ++k) {
+            if (hold && last && k == x.chunks - 1) {
+                asm volatile("bar.sync 2, %0;" ::"n"(C::THREADS) : "memory");
+                asm volatile("fence.proxy.async.global;" ::: "memory");
+                load_scales(x);
+                meta = meta_of(x);
             }
-            if (!ok) break;
-            const int s = (i + told) % C::NS, rel = lane - (told << nb_log);
-            if (rel >= 0 && rel < (1 << nb_log))
-                for (int k = 0; k < tiles; ++k)
-                    sh.meta[s * kKv8Tiles + rel * tiles + k] = make_float4(ks * p.c1, row >= 0 ? vs : -1.f, log2f(vs), 0.f);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(sh.full + s));
-            ++told;
+            if (uses > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(sh.empty + s), (uint32_t)(uses - 1) & 1u,
+                                                               p.wait_limit_ns, kSiteKv8Empty))) {
+                ok = false;
+                break;
+            }
+            copy(x, k, s, true, meta);
+            if (++s == C::NS) {
+                s = 0;
+                ++uses;
+            }
         }
-        i += ok ? f.chunks : copied;
-        f = after;
+        ahead = 0;
+        x = y;
     }
-    if (!ok)   // the copies in flight end before the block does
-        for (int k = max(0, i - C::NS); k < i; ++k)
-            mbar_wait(smem_u32(sh.full + k % C::NS), (uint32_t)(k / C::NS) & 1u, p.wait_limit_ns, kSiteKv8Full);
+    if (!ok)   // the copies in flight end before the block does: the stages' latest uses
+        for (int k = 0; k < C::NS; ++k)
+            if (uses > 0 || k < s) mbar_wait(smem_u32(sh.full + k), (uint32_t)(k < s ? uses : uses - 1) & 1u, p.wait_limit_ns, kSiteKv8Full);
 }
 
-// The consumer warps' work on chunks [c_begin, c_end) of w's item, stages from counter i on; then the warps' sums are
+// Where a warp is in the ring: chunks before the piece, the next one of the warp's set, its stage and phase.
+struct Kv8Place {
+    int i, j, s;
+    uint32_t phase;
+    bool ok;
+};
+
+// The consumer warps' work on chunks [c_begin, c_end) of w's item; then the warps' sums are
 // joined, and emit(h, d4, O, M, L) gets features 4 d4 .. of each head's sum, its reference and weight.
 template <int D, int NT, int NRG, class C, class Emit>
 __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Shared<C>& sh, const Kv8Walk& w, int c_begin,
-                                          int c_end, int& i, bool& ok, int warp, int lane, Emit emit) {
+                                          int c_end, Kv8Place& at_ring, int warp, int lane, Emit emit) {
     constexpr int NSTEP = D / 16, VW = D / 32;
     const int g = lane >> 2, t = lane & 3;
     const int rg = warp % NRG, kslot = warp / NRG;             // set of heads, share of the keys
-    const int set = kslot / kKv8Tiles % C::SETS;
     const int h_base = rg * C::HEADS;                          // this warp's first head in the group
     const uint4* q_lane = reinterpret_cast<const uint4*>(sh.q) + rg * NT * (NSTEP / 2) * 32 + lane;
     float o[NT][2 * VW][4];
@@ -651,25 +687,25 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[x][k][e] = 0.f;
     }
-    for (int c = c_begin; c < c_end; ++c, ++i) {
-        if (C::SETS > 1 && i % C::SETS != set) continue;
-        const int s = i % C::NS;
-        if (ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(sh.full + s), (uint32_t)(i / C::NS) & 1u, p.wait_limit_ns,
-                                                     kSiteKv8Full)))
-            ok = false;
-        if (!ok) break;
-        {
-            const int tile = kslot % kKv8Tiles;
-            const int pos0 = c * kKv8Chunk + 16 * tile;
-            const float4 meta = sh.meta[s * kKv8Tiles + tile];
-            // not wanted: outside the visible keys, or on a page that is not there
-            if (pos0 + 16 > w.lo && pos0 < w.n && meta.y >= 0.f)
-                kv8_tile<D, NT>(sh.ring + (2 * s) * C::TENSOR + tile * 16 * D, C::TENSOR, pos0, w.lo, w.n, meta, q_lane, o, m,
-                                l, g, t);
-        }
+    const int tile = kslot % kKv8Tiles, tile_box = tile >> (min(p.c.log_p, 6) - 4);
+    for (; at_ring.j < at_ring.i + (c_end - c_begin); at_ring.j += C::SETS) {
+        const int s = at_ring.s;
+        if (at_ring.ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(sh.full + s), at_ring.phase, p.wait_limit_ns, kSiteKv8Full)))
+            at_ring.ok = false;
+        if (!at_ring.ok) break;
+        const int pos0 = (c_begin + at_ring.j - at_ring.i) * kKv8Chunk + 16 * tile;
+        const float4 meta = sh.meta[s * kKv8Tiles + tile_box];
+        // not wanted: outside the visible keys, or on a page that is not there
+        if (pos0 + 16 > w.lo && pos0 < w.n && meta.y >= 0.f)
+            kv8_tile<D, NT>(sh.ring + (2 * s) * C::TENSOR + tile * 16 * D, C::TENSOR, pos0, w.lo, w.n, meta, q_lane, o, m, l, g, t);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(sh.empty + s));
+        if ((at_ring.s += C::SETS) >= C::NS) {
+            at_ring.s -= C::NS;
+            at_ring.phase ^= 1u;
+        }
     }
+    at_ring.i += c_end - c_begin;
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -844,8 +880,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
         return;
     }
     grid_dependency_wait();
-    bool ok = true;
-    int i = 0;
+    const int set = warp / NRG / kKv8Tiles % C::SETS;
+    Kv8Place at_ring{0, set, set, 0u, true};
     for (int u = u0; u < u1;) {
         const int end = min(u1, w.begin + w.nch);      // of its units with keys
         for (int x = (int)threadIdx.x; x < C::NTG * 8 * (D / 4); x += 256) {
@@ -858,7 +894,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
         kv8_consumers_sync();              // and the last piece's results have been read
         const bool alone = u == w.begin && end == w.begin + w.nch;
         const int slot = 2 * (int)blockIdx.x + (r0 < w.begin ? 1 : 0);
-        kv8_piece<D, NT, NRG, C>(p, sh, w, w.ch0 + (u - w.begin), w.ch0 + (end - w.begin), i, ok, warp, lane,
+        kv8_piece<D, NT, NRG, C>(p, sh, w, w.ch0 + (u - w.begin), w.ch0 + (end - w.begin), at_ring, warp, lane,
                                  [&](int h, int d4, const float4& O, float M, float L) {
                                      if (alone) {
                                          kv8_store4<D>(p, w.b, w.hk, h, d4, O, M, L);
@@ -1017,9 +1053,9 @@ __global__ void __launch_bounds__(Kv8StepCfg<D>::THREADS, 2)
             sh.q[kv8_q_place<D>(row, HALF + 4 * c)] = head ? bf16x4_to_half4(o1) : make_uint2(0u, 0u);
         }
         kv8_consumers_sync();
-        bool ok = true;
-        int i = 0;
-        kv8_piece<D, 1, 1, C>(p, sh, w, w.ch0 + u0, w.ch0 + u1, i, ok, warp, lane,
+        const int set = warp / kKv8Tiles % C::SETS;
+        Kv8Place at_ring{0, set, set, 0u, true};
+        kv8_piece<D, 1, 1, C>(p, sh, w, w.ch0 + u0, w.ch0 + u1, at_ring, warp, lane,
                               [&](int h, int d4, const float4& O, float M, float L) {
                                   if (ranks == 1) {
                                       kv8_store4<D>(p, w.b, w.hk, h, d4, O, M, L);
