@@ -9,6 +9,7 @@
 #pragma once
 
 #include <climits>
+#include <type_traits>
 
 #include "decode.cuh"
 #include "kv8.cuh"
@@ -268,8 +269,9 @@ struct Kv8Cfg {
     // Ring stages: a multiple of SETS, so that a set of warps takes every use of its stages and its waits see each
     // phase of their barriers in turn.
     static constexpr int NS = NSTAGES;
-    // one head in two of half of the warps' results
-    static constexpr int MERGE = CONSUMERS / 2 * (HEADS / 2) * D * 4;
+    // Results on their way to be joined: one head in two of half of the warps, or two heads of each warp.
+    static constexpr int MERGE_PITCH = D + 16;
+    static constexpr int MERGE = CONSUMERS / 2 * (HEADS / 2) * MERGE_PITCH * 4;
     static constexpr int OFF_O = NS * 2 * TENSOR;
     static constexpr int OFF_ML = OFF_O + MERGE;                 // m [8][HEADS], l [8][HEADS]
     static constexpr int OFF_Q = OFF_ML + 2 * CONSUMERS * HEADS * 4;      // qhat as fp16 operands
@@ -303,8 +305,12 @@ struct Kv8Walk {
     __device__ __forceinline__ int size() const { return nch + kKv8ItemCost; }
 
     __device__ __forceinline__ void load(const Kv8AttnParams& p) {
-        n = kv8_length(p.seq_len, b, p.max_pages, p.c.log_p);
-        lo = n > 0 ? kv8_first_key(p, b, n) : 0;
+        const int len = kv8_length(p.seq_len, b, p.max_pages, p.c.log_p);
+        set(len, len > 0 ? kv8_first_key(p, b, len) : 0);
+    }
+    __device__ __forceinline__ void set(int n_, int lo_) {
+        n = n_;
+        lo = lo_;
         ch0 = lo / kKv8Chunk;
         nch = n > 0 ? (n - 1) / kKv8Chunk - ch0 + 1 : 0;
     }
@@ -712,11 +718,14 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
         for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], d);
-    // The heads of one parity at a time, for the buffer's sake: half of the warps put theirs down, the others add them to
-    // their own and put those down.
-    constexpr int HH = C::HEADS / 2, KH = C::KSLOTS / 2;
-    const bool upper = warp >= C::CONSUMERS / 2;
-    const int place = (upper ? warp - C::CONSUMERS / 2 : warp) * HH;
+    // The warps' sums, the heads of one parity at a time (the buffer holds no more).  With at most four heads every warp
+    // puts its own down; with more, half of the warps do, and the others add them to theirs and put those down.
+    // A head's features lie in the buffer as [pair][g][2], so that a warp's stores meet no bank twice.
+    constexpr int HH = C::HEADS / 2, PITCH = C::MERGE_PITCH;
+    const bool direct = NT == 1 && p.G <= 4;
+    const bool upper = !direct && warp >= C::CONSUMERS / 2;
+    const int per_warp = direct ? 2 : HH;                       // places of a warp
+    const int place = (upper ? warp - C::CONSUMERS / 2 : warp) * per_warp;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         if (e == 1 && p.G == 1) break;
@@ -731,55 +740,65 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
                 }
 #pragma unroll
                 for (int k = 0; k < 2 * VW; ++k)
-                    *reinterpret_cast<float2*>(sh.o + at * D + 4 * VW * g + 2 * k) = make_float2(o[x][k][e], o[x][k][2 + e]);
+                    *reinterpret_cast<float2*>(sh.o + at * PITCH + 16 * k + 2 * g) = make_float2(o[x][k][e], o[x][k][2 + e]);
             }
         };
         if (e == 1) kv8_consumers_sync();  // the other parity has been read
-        if (upper) put();
+        if (direct || upper) put();
         kv8_consumers_sync();
-        if (!upper) {
+        if (!direct) {
+            if (!upper) {
 #pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                if (h_base + 8 * x + 2 * t + e >= p.G) continue;
-                const int at = place + 4 * x + t;
-                const float m2 = sh.m[at], l2 = sh.l[at];
-                const float M = fmaxf(m[x][e], m2);
-                const float f1 = kv8_factor(m[x][e], l[x][e], M), f2 = kv8_factor(m2, l2, M);
+                for (int x = 0; x < NT; ++x) {
+                    if (h_base + 8 * x + 2 * t + e >= p.G) continue;
+                    const int at = place + 4 * x + t;
+                    const float m2 = sh.m[at], l2 = sh.l[at];
+                    const float M = fmaxf(m[x][e], m2);
+                    const float f1 = kv8_factor(m[x][e], l[x][e], M), f2 = kv8_factor(m2, l2, M);
 #pragma unroll
-                for (int k = 0; k < 2 * VW; ++k) {
-                    const float2 o2 = *reinterpret_cast<const float2*>(sh.o + at * D + 4 * VW * g + 2 * k);
-                    o[x][k][e] = o[x][k][e] * f1 + o2.x * f2;
-                    o[x][k][2 + e] = o[x][k][2 + e] * f1 + o2.y * f2;
+                    for (int k = 0; k < 2 * VW; ++k) {
+                        const float2 o2 = *reinterpret_cast<const float2*>(sh.o + at * PITCH + 16 * k + 2 * g);
+                        o[x][k][e] = o[x][k][e] * f1 + o2.x * f2;
+                        o[x][k][2 + e] = o[x][k][2 + e] * f1 + o2.y * f2;
+                    }
+                    m[x][e] = M;
+                    l[x][e] = l[x][e] * f1 + l2 * f2;
                 }
-                m[x][e] = M;
-                l[x][e] = l[x][e] * f1 + l2 * f2;
+                __syncwarp();
+                put();                     // where it has just read
             }
-            __syncwarp();
-            put();                         // where it has just read
+            kv8_consumers_sync();
         }
-        kv8_consumers_sync();
-        const int n_heads = (p.G + 1 - e) / 2;                  // heads 2 y + e
-        for (int x = (int)threadIdx.x; x < n_heads * (D / 4); x += 256) {
-            const int y = x / (D / 4), d4 = x % (D / 4);
-            const int r = y / HH, yc = y % HH;
-            float M = -INFINITY;
+        // SLOTS results of each head, STEP places apart
+        auto join = [&](auto slots, auto stride) {
+            constexpr int SLOTS = decltype(slots)::value, STEP = decltype(stride)::value;
+            const int n_heads = (p.G + 1 - e) / 2;              // heads 2 y + e
+            for (int x = (int)threadIdx.x; x < n_heads * (D / 4); x += 256) {
+                const int y = x / (D / 4), d4 = x % (D / 4);
+                float mk[SLOTS], M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int k = 0; k < KH; ++k) M = fmaxf(M, sh.m[(k * NRG + r) * HH + yc]);
-            float L = 0.f;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < SLOTS; ++k) {
+                    mk[k] = sh.m[y + k * STEP];
+                    M = fmaxf(M, mk[k]);
+                }
+                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float* src = sh.o + y * PITCH + 16 * (2 * (d4 % VW)) + 2 * (d4 / VW);
 #pragma unroll
-            for (int k = 0; k < KH; ++k) {
-                const int at = (k * NRG + r) * HH + yc;
-                const float f = kv8_factor(sh.m[at], sh.l[at], M);
-                const float4 v = *reinterpret_cast<const float4*>(sh.o + at * D + 4 * d4);
-                L = fmaf(sh.l[at], f, L);
-                O.x = fmaf(v.x, f, O.x);
-                O.y = fmaf(v.y, f, O.y);
-                O.z = fmaf(v.z, f, O.z);
-                O.w = fmaf(v.w, f, O.w);
+                for (int k = 0; k < SLOTS; ++k) {
+                    const float lk = sh.l[y + k * STEP], f = kv8_factor(mk[k], lk, M);
+                    const float2 a = *reinterpret_cast<const float2*>(src + k * STEP * PITCH);
+                    const float2 b = *reinterpret_cast<const float2*>(src + k * STEP * PITCH + 16);
+                    L = fmaf(lk, f, L);
+                    O.x = fmaf(a.x, f, O.x);
+                    O.y = fmaf(a.y, f, O.y);
+                    O.z = fmaf(b.x, f, O.z);
+                    O.w = fmaf(b.y, f, O.w);
+                }
+                emit(2 * y + e, d4, O, M, L);
             }
-            emit(2 * y + e, d4, O, M, L);
-        }
+        };
+        if (direct) join(std::integral_constant<int, C::CONSUMERS>{}, std::integral_constant<int, 2>{});
+        else join(std::integral_constant<int, C::KSLOTS / 2>{}, std::integral_constant<int, NRG * HH>{});
     }
 }
 
@@ -805,14 +824,10 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
     extern __shared__ __align__(1024) uint8_t dsmem[];
     const Kv8Shared<C> sh(dsmem);
     __shared__ int s_warp_sum[C::CONSUMERS + 1];
-    __shared__ int s_from[4], s_to, s_last;
+    __shared__ int s_from[6], s_to, s_last;
+    __shared__ volatile int s_walk[2][8], s_units[2];
 
     const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31u);
-    if (threadIdx.x == 0) {
-        sh.init_barriers();
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
-    }
     // this block's units: chunks before each request, summed over a slice of the requests per thread
     Kv8Walk w;
     const int per = (p.B + C::THREADS - 1) / C::THREADS;
@@ -821,6 +836,11 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
     for (w.b = b_lo; w.b < b_hi; ++w.b) {
         w.load(p);
         if (w.nch > 0) mine += w.size();
+    }
+    if (threadIdx.x == 32 * C::CONSUMERS) {
+        sh.init_barriers();
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
     }
     int incl = mine;
 #pragma unroll
@@ -839,6 +859,10 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
     const int n_units = total * p.c.Hkv;
     const int n_blocks = min((int)gridDim.x, (n_units + kKv8MinShare - 1) / kKv8MinShare);
     if ((int)blockIdx.x >= n_blocks) return;
+    if (threadIdx.x == 0) {
+        s_units[0] = n_units;
+        s_units[1] = n_blocks;
+    }
     const Kv8Shares shares(n_units, n_blocks);
     // Where this block's stretch begins and ends: a boundary inside a small item, or among the units of an item's
     // cost, moves to that item's end.
@@ -850,7 +874,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
         if (r >= incl * p.c.Hkv || r < (incl - mine) * p.c.Hkv) continue;
         int before = incl - mine;
         for (w.b = b_lo;; ++w.b) {
-            w.load(p);
+            if (per > 1) w.load(p);
             if (w.nch == 0) continue;
             if (r < (before + w.size()) * p.c.Hkv) break;
             before += w.size();
@@ -862,6 +886,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
             s_from[1] = hk;
             s_from[2] = begin;
             s_from[3] = at;
+            s_from[4] = w.n;
+            s_from[5] = w.lo;
         } else {
             s_to = at;
         }
@@ -872,7 +898,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
     w.b = s_from[0];
     w.hk = s_from[1];
     w.begin = s_from[2];
-    w.load(p);
+    w.set(s_from[4], s_from[5]);
     if (u0 == w.begin + w.size()) w.next(p);
 
     if (warp == C::CONSUMERS) {
@@ -882,8 +908,9 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
     grid_dependency_wait();
     const int set = warp / NRG / kKv8Tiles % C::SETS;
     Kv8Place at_ring{0, set, set, 0u, true};
-    for (int u = u0; u < u1;) {
-        const int end = min(u1, w.begin + w.nch);      // of its units with keys
+    int turn = 0;
+    for (int u = u0; u < s_to; turn ^= 1) {
+        const int end = min(s_to, w.begin + w.nch);    // of its units with keys
         for (int x = (int)threadIdx.x; x < C::NTG * 8 * (D / 4); x += 256) {
             const int h = x / (D / 4), f = 4 * (x % (D / 4));
             uint2 raw = make_uint2(0u, 0u);
@@ -891,27 +918,44 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
                 raw = *reinterpret_cast<const uint2*>(p.qh + ((long long)w.b * p.H + (long long)w.hk * p.G + h) * D + f);
             sh.q[kv8_q_place<D>(h, f)] = bf16x4_to_half4(raw);
         }
+        // The walk goes through shared memory over the loop on the keys, which needs every register; in turn, so that a
+        // warp that is behind still finds its piece's.
+        volatile int* at = s_walk[turn];
+        if (threadIdx.x == 0) {
+            at[0] = w.b;
+            at[1] = w.hk;
+            at[2] = w.begin;
+            at[3] = end;
+            at[4] = u == w.begin && end == w.begin + w.nch;            // the item is this block's alone
+            at[5] = 2 * (int)blockIdx.x + (r0 < w.begin ? 1 : 0);      // else: the piece's place
+        }
         kv8_consumers_sync();              // and the last piece's results have been read
-        const bool alone = u == w.begin && end == w.begin + w.nch;
-        const int slot = 2 * (int)blockIdx.x + (r0 < w.begin ? 1 : 0);
         kv8_piece<D, NT, NRG, C>(p, sh, w, w.ch0 + (u - w.begin), w.ch0 + (end - w.begin), at_ring, warp, lane,
                                  [&](int h, int d4, const float4& O, float M, float L) {
-                                     if (alone) {
-                                         kv8_store4<D>(p, w.b, w.hk, h, d4, O, M, L);
+                                     if (at[4]) {
+                                         kv8_store4<D>(p, at[0], at[1], h, d4, O, M, L);
                                      } else {
-                                         float* pt = p.part + ((long long)slot * p.G + h) * (D + 4);
+                                         float* pt = p.part + ((long long)at[5] * p.G + h) * (D + 4);
                                          *reinterpret_cast<float4*>(pt + 4 * d4) = O;
                                          if (d4 == 0) *reinterpret_cast<float2*>(pt + D) = make_float2(M, L);
                                      }
                                  });
-        if (!alone) {
+        w.b = at[0];
+        w.hk = at[1];
+        w.begin = at[2];
+        w.set(w.n, w.lo);
+        if (!at[4]) {
+            const Kv8Shares shares(s_units[0], s_units[1]);
             const int c_first = shares.owner(w.begin);
             const int pieces = shares.owner(w.begin + w.nch - 1) - c_first + 1;
             kv8_consumers_sync();
-            if (threadIdx.x == 0) {        // releases the block's piece, and takes in the others'
-                __threadfence();
-                s_last = atomicAdd(p.counters + c_first, 1) == pieces - 1;
-                __threadfence();
+            if (threadIdx.x == 0) {        // releases the block's piece (the barrier before it), acquires the others'
+                int arrived;
+                asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                             : "=r"(arrived)
+                             : "l"(p.counters + c_first)
+                             : "memory");
+                s_last = arrived == pieces - 1;
             }
             kv8_consumers_sync();
             if (s_last) {
@@ -989,8 +1033,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
                 kv8_consumers_sync();      // before the buffer is written again
             }
         }
-        u = end == w.begin + w.nch ? w.begin + w.size() : end;
-        if (u < u1) w.next(p);
+        u = at[3] == w.begin + w.nch ? w.begin + w.size() : at[3];
+        if (u < s_to) w.next(p);
     }
 }
 
