@@ -27,7 +27,7 @@ struct Kv8TokenParams {
     const __nv_bfloat16* Wg;
     const int* table;             // (B, max_pages)
     const int* seq_len;           // (B)
-    __nv_bfloat16* qh;            // (B, H, D), workspace
+    uint2* qh;                    // (B, Hkv) items of qhat as operands (kv8_q_place), workspace
     __nv_bfloat16* out;           // (B, H, D): the empty rows are written here
     float* lse;                   // (B, H) or null
     Kv8Store c;
@@ -160,6 +160,24 @@ struct Kv8Row {
     }
 };
 
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Place, in groups of four, of features f .. f + 3 (f a multiple of 4) of head h among an item's heads of qhat as the
+// products' B operands, fp16: lane t of a quad takes D/4 consecutive features (kv8_tile), eight of them from each 16 bytes;
+// [head][eights][t].
+template <int D>
+__device__ __forceinline__ int kv8_q_place(int h, int f) {
+    constexpr int EIGHTS = D / 32;                              // of a lane
+    const int eight = f / 8;
+    return ((h * EIGHTS + eight % EIGHTS) * 4 + eight / EIGHTS) * 2 + (f & 4) / 4;
+}
+__device__ __forceinline__ uint2 bf16x4_to_half4(uint2 raw) {
+    return make_uint2(pack_half2(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u)),
+                      pack_half2(__uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)));
+}
+
 // Rows of request b = blockIdx.x: its H query rows, then its Hkv key/value rows (when the token is to be
 // appended); blockIdx.y takes one group of 256 / (D/8) rows.  Every block builds the RoPE row of the token's
 // position in shared memory.
@@ -189,9 +207,10 @@ __global__ void __launch_bounds__(256) kv8_token_kernel(const Kv8TokenParams p) 
     uint2 o0, o1;
     r.finish(p, n - 1, c, s_tab32, s_tab64, o0, o1);
     if (is_q) {
-        __nv_bfloat16* dst = p.qh + ((long long)b * p.H + row) * D + 4 * c;
-        *reinterpret_cast<uint2*>(dst) = o0;
-        *reinterpret_cast<uint2*>(dst + HALF) = o1;
+        const int G = p.H / p.c.Hkv, item = row / G, h = row - item * G;
+        uint2* dst = p.qh + ((long long)b * p.c.Hkv + item) * (G * D / 4);
+        dst[kv8_q_place<D>(h, 4 * c)] = bf16x4_to_half4(o0);
+        dst[kv8_q_place<D>(h, HALF + 4 * c)] = bf16x4_to_half4(o1);
     }
 }
 
@@ -241,7 +260,7 @@ constexpr float kSlack = 10.f;          // fp16 holds 2^15
 enum : unsigned int { kSiteKv8Full = 83, kSiteKv8Empty = 84 };
 
 struct Kv8AttnParams {
-    const __nv_bfloat16* qh;      // (B, H, D)
+    const uint2* qh;              // (B, Hkv) items of qhat as operands (kv8_q_place)
     const int* table;
     const int* seq_len;
     const int* doc_start;         // (B) or null
@@ -259,10 +278,10 @@ struct Kv8AttnParams {
 template <int D, int NT, int NRG, int NSTAGES>
 struct Kv8Cfg {
     static constexpr int CONSUMERS = 8;
-    static constexpr int THREADS = 32 * (CONSUMERS + 1);
     static constexpr int BLOCKS_PER_SM = NT == 1 ? 2 : 1;
     static constexpr int KSLOTS = CONSUMERS / NRG;               // warps that share the keys of a group of heads
-    static constexpr int SETS = KSLOTS / kKv8Tiles;              // chunks in work at a time
+    static constexpr int SETS = KSLOTS / kKv8Tiles;              // chunks in work at a time, each set with a producer warp
+    static constexpr int THREADS = 32 * (CONSUMERS + SETS);
     static constexpr int TENSOR = kKv8Chunk * D;                 // bytes of a chunk's K (and V)
     static constexpr int HEADS = 8 * NT;                         // query heads of a warp
     static constexpr int NTG = NT * NRG;                         // groups of eight heads
@@ -274,10 +293,12 @@ struct Kv8Cfg {
     static constexpr int MERGE = CONSUMERS / 2 * (HEADS / 2) * MERGE_PITCH * 4;
     static constexpr int OFF_O = NS * 2 * TENSOR;
     static constexpr int OFF_ML = OFF_O + MERGE;                 // m [8][HEADS], l [8][HEADS]
-    static constexpr int OFF_Q = OFF_ML + 2 * CONSUMERS * HEADS * 4;      // qhat as fp16 operands
-    static constexpr int OFF_META = OFF_Q + NTG * 8 * D * 2;     // per stage and tile: ks c1, vs, log2 vs, pad
+    static constexpr int OFF_Q = OFF_ML + 2 * CONSUMERS * HEADS * 4;      // items' qhat operands: two of the largest, or more
+    static constexpr int QBYTES = 2 * NTG * 8 * D * 2;
+    static constexpr int MAXQ = 8;                               // items in that ring, at most
+    static constexpr int OFF_META = OFF_Q + QBYTES;              // per stage and tile: ks c1, vs, log2 vs, pad
     static constexpr int OFF_BAR = OFF_META + NS * kKv8Tiles * 16;
-    static constexpr int SMEM = OFF_BAR + 2 * NS * 8 + 1024;     // + alignment slack
+    static constexpr int SMEM = OFF_BAR + 2 * (NS + MAXQ) * 8 + 1024;     // + alignment slack
     static_assert(NS % SETS == 0, "a stage belongs to one set of warps");
     static_assert(MERGE >= 4096, "the sums of a shared item's pieces");
     static_assert(BLOCKS_PER_SM * (SMEM + 2048) <= 228 * 1024, "shared memory");
@@ -343,10 +364,6 @@ __device__ __forceinline__ void fp8x4_to_half4(uint32_t four, uint32_t& lo, uint
         : "=r"(lo), "=r"(hi)
         : "r"(four));
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 // 8x8 matrix of 16-bit elements held two to a lane (row lane / 4), transposed.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t r;
@@ -365,10 +382,11 @@ __device__ __forceinline__ float kv8_factor(float m, float l, float M) {
 }
 
 // One tile of 16 keys at position pos0, rows at kr (and `tensor` bytes behind it the values), for NT groups of eight
-// heads.  meta: key scale times c1, value scale, its log2.  q: this lane's qhat operands, two steps in each 16 bytes.
+// heads.  meta: key scale times c1, value scale, its log2.  q: this lane's qhat operands, of each group's head,
+// 16-byte words four apart.
 template <int D, int NT>
 __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0, int lo, int n, const float4& meta,
-                                         const uint4* q, float (&o)[NT][D / 16][4], float (&m)[NT][2],
+                                         const uint4* const (&q)[NT], float (&o)[NT][D / 16][4], float (&m)[NT][2],
                                          float (&l)[NT][2], int g, int t) {
     constexpr int NSTEP = D / 16, VW = D / 32;
     const bool whole = pos0 >= lo && pos0 + 16 <= n;
@@ -398,7 +416,7 @@ __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0
     for (int st = 0; st < NSTEP; ++st) {
         if ((st & 1) == 0)
 #pragma unroll
-            for (int x = 0; x < NT; ++x) qs[x] = q[(x * (NSTEP / 2) + st / 2) * 32];
+            for (int x = 0; x < NT; ++x) qs[x] = q[x][st / 2 * 4];
         uint32_t a0, a1, a2, a3;
         fp8x4_to_half4(a[0][st], a0, a2);
         fp8x4_to_half4(a[1][st], a1, a3);
@@ -508,53 +526,72 @@ struct Kv8Shared {
     float* o;
     float* m;
     float* l;
-    uint2* q;
+    uint4* q;
     float4* meta;
     uint64_t* full;
     uint64_t* empty;
+    uint64_t* q_full;
+    uint64_t* q_empty;
 
     __device__ __forceinline__ explicit Kv8Shared(uint8_t* dsmem) {
         ring = dsmem + ((1024u - (smem_u32(dsmem) & 1023u)) & 1023u);
         o = reinterpret_cast<float*>(ring + C::OFF_O);
         m = reinterpret_cast<float*>(ring + C::OFF_ML);
         l = m + C::CONSUMERS * C::HEADS;
-        q = reinterpret_cast<uint2*>(ring + C::OFF_Q);
+        q = reinterpret_cast<uint4*>(ring + C::OFF_Q);
         meta = reinterpret_cast<float4*>(ring + C::OFF_META);
         full = reinterpret_cast<uint64_t*>(ring + C::OFF_BAR);
         empty = full + C::NS;
+        q_full = empty + C::NS;
+        q_empty = q_full + C::MAXQ;
+    }
+    // Items in the ring of qhat operands, each of G * D / 8 16-byte words: a power of two.
+    static __device__ __forceinline__ int q_ring_log(int words) {
+        return 31 - __clz(min(C::MAXQ, C::QBYTES / (16 * words)));
     }
     __device__ __forceinline__ void init_barriers() const {
         for (int s = 0; s < C::NS; ++s) {
-            mbar_init(smem_u32(full + s), 2);
+            mbar_init(smem_u32(full + s), 1);
             mbar_init(smem_u32(empty + s), C::CONSUMERS / C::SETS);
+        }
+        for (int s = 0; s < C::MAXQ; ++s) {
+            mbar_init(smem_u32(q_full + s), 1);
+            mbar_init(smem_u32(q_empty + s), C::CONSUMERS);
         }
         fence_barrier_init();
     }
 };
 
-// The producer warp: the chunks of units [u0, u1) from walk position w into the ring.  box {D, min(P, 64)}.
-// kAppend: the block itself writes the new token (the threads that do so arrive at barrier 2), so the item's last chunk
-// waits for that.
+// A producer warp: its set's chunks (every SETS-th, from `part` on) of units [u0, u1) from walk position w into the ring; one
+// warp for all chunks would bound a block at D = 64.  Box {D, min(P, 64)}.
+// kAppend: the block itself writes the new token (the consumers arrive at barrier 2 when that is done), so the item's last
+// chunk waits for that.
 template <int D, class C, bool kAppend>
 __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Kv8AttnParams& p,
-                                            const Kv8Shared<C>& sh, Kv8Walk w, int u0, int u1, int lane, bool append) {
+                                            const Kv8Shared<C>& sh, Kv8Walk w, int u0, int u1, int part, int lane,
+                                            bool append) {
     // A box is a page, or the half of a 128-token page that a chunk has.
     const int box_log = min(p.c.log_p, 6), nb_log = 6 - box_log;   // 64 >> nb_log keys; boxes of a chunk
     const uint32_t box_bytes = (uint32_t)((1 << box_log) * D);
     // A batch: the boxes, one to a lane, of up to 32 >> nb_log chunks of an item.  Its table entries are loaded two
-    // batches ahead, its scales one: one warp feeds the block, and what it spends on a chunk bounds the block's rate.
+    // batches ahead, its scales one: what the warp spends on a chunk bounds the rate of its set.
     struct Pages {
         int chunks, hk, page, sub;     // this lane's table entry (kNone: not wanted), its first row in the page
+        int item;                      // whose first chunks here these are, else -1
     };
     struct Boxes {
         int chunks, ph, row;           // this lane's page and head, and its first row in the cache (-1: none)
+        int item;
         float ks, vs;
     };
     constexpr int kNone = INT_MIN;
     int u = u0, c = w.ch0 + (u0 - w.begin);
+    bool fresh = true;
     auto look_up = [&]() {
-        Pages f{0, w.hk, kNone, 0};
+        Pages f{0, w.hk, kNone, 0, -1};
         if (u >= u1) return f;
+        if (fresh) f.item = w.b * p.c.Hkv + w.hk;
+        fresh = false;
         const int c_end = w.ch0 + (min(u1, w.begin + w.nch) - w.begin);
         f.chunks = min(32 >> nb_log, c_end - c);
         const long long pos = (long long)c * kKv8Chunk + ((long long)lane << box_log);
@@ -569,6 +606,7 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
         if (c == c_end && u < u1) {
             w.next(p);
             c = w.ch0;
+            fresh = true;
         }
         return f;
     };
@@ -579,7 +617,7 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
         }
     };
     auto find = [&](const Pages& f) {
-        Boxes x{f.chunks, 0, -1, 0.f, -1.f};
+        Boxes x{f.chunks, 0, -1, f.item, 0.f, -1.f};
         if (f.page >= 0 && f.page < p.c.n_pages) {
             x.ph = f.page * p.c.Hkv + f.hk;
             x.row = (x.ph << p.c.log_p) + f.sub;
@@ -589,18 +627,25 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
         }
         return x;
     };
-    int s = 0, uses = 0;               // the next stage, and how often the ring has gone round
-    // Chunk k's copies into stage `st`; its scales.
-    auto copy = [&](const Boxes& x, int k, int st, bool with_scales, const float4& meta) {
+    int next = part, s = part, uses = 0;   // the set's next chunk, from the batch's first; its stage; how often round the ring
+    auto advance = [&]() {
+        next += C::SETS;
+        if ((s += C::SETS) >= C::NS) {
+            s -= C::NS;
+            ++uses;
+        }
+    };
+    // Chunk k's copies into stage st, with its scales where `meta` is given.
+    auto copy = [&](const Boxes& x, int k, int st, const float4* meta) {
         const int rel = lane - (k << nb_log);
         const bool here = (unsigned)rel < (1u << nb_log), load = here && x.row >= 0;
-        if (with_scales && here) sh.meta[st * kKv8Tiles + rel] = meta;
+        if (meta != nullptr && here) sh.meta[st * kKv8Tiles + rel] = *meta;
         const uint32_t n_load = (uint32_t)__popc(__ballot_sync(0xffffffffu, load));
         const uint32_t bar = smem_u32(sh.full + st);
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive_expect_tx(bar, n_load * 2u * box_bytes);
-            if (with_scales) mbar_arrive(bar);
+            if (meta != nullptr) mbar_arrive_expect_tx(bar, n_load * 2u * box_bytes);
+            else asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n_load * 2u * box_bytes) : "memory");
         }
         __syncwarp();
         if (load) {
@@ -608,6 +653,29 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
             tma_load_2d(dst, &tm_k, bar, 0, x.row);
             tma_load_2d(dst + C::TENSOR, &tm_v, bar, 0, x.row);
         }
+    };
+    // An item's qhat (of the token kernel).
+    const int q_words = p.G * D / 8, q_ring = 1 << Kv8Shared<C>::q_ring_log(q_words);
+    int qs = 0, q_uses = 0;
+    auto copy_q = [&](int item) {
+        if (kAppend || part > 0 || item < 0) return true;
+        if (q_uses > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(sh.q_empty + qs), (uint32_t)(q_uses - 1) & 1u,
+                                                             p.wait_limit_ns, kSiteKv8Empty)))
+            return false;
+        if (lane == 0) {
+            const uint32_t bar = smem_u32(sh.q_full + qs);
+            mbar_arrive_expect_tx(bar, (uint32_t)q_words * 16u);
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem_u32(sh.q + qs * q_words)),
+                         "l"(p.qh + (long long)item * (2 * q_words)), "r"(q_words * 16), "r"(bar)
+                         : "memory");
+        }
+        __syncwarp();
+        if (++qs == q_ring) {
+            qs = 0;
+            ++q_uses;
+        }
+        return true;
     };
     auto meta_of = [&](const Boxes& x) { return make_float4(x.ks * p.c1, x.row >= 0 ? x.vs : -1.f, log2f(x.vs), 0.f); };
 
@@ -619,29 +687,32 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
     }
     Boxes x = find(f);
     f = look_up();
-    // the first copies do not wait for the scales
+    // the first copies, into an empty ring, do not wait for the scales
     const bool hold = kAppend && append;                       // the last chunk waits for the block's own token
-    int ahead = min(x.chunks - (hold && f.chunks == 0 ? 1 : 0), C::NS);
-    for (int k = 0; k < ahead; ++k) copy(x, k, k, false, make_float4(0.f, 0.f, 0.f, 0.f));
+    const int ahead = min(x.chunks - (hold && f.chunks == 0 ? 1 : 0), C::NS);
+    copy_q(x.item);
+    x.item = -1;
+    for (int k = part; k < ahead; k += C::SETS) copy(x, k, k, nullptr);
+    float4 meta = meta_of(x);
+    while (next < ahead) {
+        const int rel = lane - (next << nb_log);
+        if ((unsigned)rel < (1u << nb_log)) sh.meta[s * kKv8Tiles + rel] = meta;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(sh.full + s));
+        advance();
+    }
     bool ok = true;
-    while (x.chunks > 0 && ok) {
-        float4 meta = meta_of(x);
-        for (int k = 0; k < ahead; ++k) {
-            const int rel = lane - (k << nb_log);
-            if ((unsigned)rel < (1u << nb_log)) sh.meta[k * kKv8Tiles + rel] = meta;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(sh.full + k));
-            if (++s == C::NS) {
-                s = 0;
-                ++uses;
-            }
-        }
+    while (x.chunks > 0) {
         const bool last = f.chunks == 0;
         const Boxes y = find(f);
         f = look_up();
-        for (int k = ahead; k < x.chunks; ++k) {
-            if (hold && last && k == x.chunks - 1) {
-                asm volatile("bar.sync 2, %0;" ::"n"(C::THREADS) : "memory");
+        if (!copy_q(x.item)) {
+            ok = false;
+            break;
+        }
+        while (next < x.chunks) {
+            if (hold && last && next == x.chunks - 1) {
+                asm volatile("bar.sync 2, %0;" ::"n"(32 * (C::CONSUMERS + 1)) : "memory");
                 asm volatile("fence.proxy.async.global;" ::: "memory");
                 load_scales(x);
                 meta = meta_of(x);
@@ -651,23 +722,27 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
                 ok = false;
                 break;
             }
-            copy(x, k, s, true, meta);
-            if (++s == C::NS) {
-                s = 0;
-                ++uses;
-            }
+            copy(x, next, s, &meta);
+            advance();
         }
-        ahead = 0;
+        if (!ok) break;
+        next -= x.chunks;
         x = y;
+        meta = meta_of(x);
     }
     if (!ok)   // the copies in flight end before the block does: the stages' latest uses
-        for (int k = 0; k < C::NS; ++k)
-            if (uses > 0 || k < s) mbar_wait(smem_u32(sh.full + k), (uint32_t)(k < s ? uses : uses - 1) & 1u, p.wait_limit_ns, kSiteKv8Full);
+        for (int k = part; k < C::NS; k += C::SETS)
+            if (uses > 0 || k < s)
+                mbar_wait(smem_u32(sh.full + k), (uint32_t)(k < s ? uses : uses - 1) & 1u, p.wait_limit_ns, kSiteKv8Full);
+    if (!ok && !kAppend && part == 0)
+        for (int k = 0; k < q_ring; ++k)
+            if (q_uses > 0 || k < qs)
+                mbar_wait(smem_u32(sh.q_full + k), (uint32_t)(k < qs ? q_uses : q_uses - 1) & 1u, p.wait_limit_ns, kSiteKv8Full);
 }
 
-// Where a warp is in the ring: chunks before the piece, the next one of the warp's set, its stage and phase.
+// Where a warp is in the ring: the next chunk of its set, counted from the piece's first, its stage and phase.
 struct Kv8Place {
-    int i, j, s;
+    int next, s;
     uint32_t phase;
     bool ok;
 };
@@ -676,12 +751,15 @@ struct Kv8Place {
 // joined, and emit(h, d4, O, M, L) gets features 4 d4 .. of each head's sum, its reference and weight.
 template <int D, int NT, int NRG, class C, class Emit>
 __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Shared<C>& sh, const Kv8Walk& w, int c_begin,
-                                          int c_end, Kv8Place& at_ring, int warp, int lane, Emit emit) {
-    constexpr int NSTEP = D / 16, VW = D / 32;
+                                          int c_end, Kv8Place& at_ring, volatile int* turn, int q_log, int warp, int lane,
+                                          Emit emit) {
+    constexpr int VW = D / 32;
     const int g = lane >> 2, t = lane & 3;
     const int rg = warp % NRG, kslot = warp / NRG;             // set of heads, share of the keys
     const int h_base = rg * C::HEADS;                          // this warp's first head in the group
-    const uint4* q_lane = reinterpret_cast<const uint4*>(sh.q) + rg * NT * (NSTEP / 2) * 32 + lane;
+    const uint4* q[NT];                                        // heads past the group repeat its last one
+#pragma unroll
+    for (int x = 0; x < NT; ++x) q[x] = sh.q + ((*turn & ((1 << q_log) - 1)) * p.G + min(h_base + 8 * x + g, p.G - 1)) * (D / 8) + t;
     float o[NT][2 * VW][4];
     float m[NT][2], l[NT][2];                                  // heads 2 t and 2 t + 1 of each group
 #pragma unroll
@@ -694,16 +772,17 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
             for (int e = 0; e < 4; ++e) o[x][k][e] = 0.f;
     }
     const int tile = kslot % kKv8Tiles, tile_box = tile >> (min(p.c.log_p, 6) - 4);
-    for (; at_ring.j < at_ring.i + (c_end - c_begin); at_ring.j += C::SETS) {
+    const int n_chunks = c_end - c_begin, first_pos = c_begin * kKv8Chunk + 16 * tile;
+    for (; at_ring.next < n_chunks; at_ring.next += C::SETS) {
         const int s = at_ring.s;
         if (at_ring.ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(sh.full + s), at_ring.phase, p.wait_limit_ns, kSiteKv8Full)))
             at_ring.ok = false;
         if (!at_ring.ok) break;
-        const int pos0 = (c_begin + at_ring.j - at_ring.i) * kKv8Chunk + 16 * tile;
+        const int pos0 = first_pos + at_ring.next * kKv8Chunk;
         const float4 meta = sh.meta[s * kKv8Tiles + tile_box];
         // not wanted: outside the visible keys, or on a page that is not there
         if (pos0 + 16 > w.lo && pos0 < w.n && meta.y >= 0.f)
-            kv8_tile<D, NT>(sh.ring + (2 * s) * C::TENSOR + tile * 16 * D, C::TENSOR, pos0, w.lo, w.n, meta, q_lane, o, m, l, g, t);
+            kv8_tile<D, NT>(sh.ring + (2 * s) * C::TENSOR + tile * 16 * D, C::TENSOR, pos0, w.lo, w.n, meta, q, o, m, l, g, t);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(sh.empty + s));
         if ((at_ring.s += C::SETS) >= C::NS) {
@@ -711,7 +790,10 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
             at_ring.phase ^= 1u;
         }
     }
-    at_ring.i += c_end - c_begin;
+    at_ring.next -= n_chunks;
+    const int piece = *turn;                                   // pieces before this one
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(sh.q_empty + (piece & ((1 << q_log) - 1))));
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -719,13 +801,15 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], d);
     // The warps' sums, the heads of one parity at a time (the buffer holds no more).  With at most four heads every warp
-    // puts its own down; with more, half of the warps do, and the others add them to theirs and put those down.
+    // puts its own down; with more, half of the warps do, and the others add them to theirs and put those down.  One head
+    // takes half of the buffer, in turn, so that warps need not wait for those that read the last piece's.
     // A head's features lie in the buffer as [pair][g][2], so that a warp's stores meet no bank twice.
     constexpr int HH = C::HEADS / 2, PITCH = C::MERGE_PITCH;
-    const bool direct = NT == 1 && p.G <= 4;
+    const bool direct = NT == 1 && p.G <= 4, one = NT == 1 && p.G == 1;
     const bool upper = !direct && warp >= C::CONSUMERS / 2;
-    const int per_warp = direct ? 2 : HH;                       // places of a warp
-    const int place = (upper ? warp - C::CONSUMERS / 2 : warp) * per_warp;
+    const int first = one ? (piece & 1) * C::CONSUMERS : 0;
+    const int place = first + (upper ? warp - C::CONSUMERS / 2 : warp) * (one ? 1 : direct ? 2 : HH);
+    const int reader = one ? ((int)threadIdx.x + 32 * piece) & 255 : (int)threadIdx.x;    // another warp each time
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         if (e == 1 && p.G == 1) break;
@@ -743,7 +827,7 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
                     *reinterpret_cast<float2*>(sh.o + at * PITCH + 16 * k + 2 * g) = make_float2(o[x][k][e], o[x][k][2 + e]);
             }
         };
-        if (e == 1) kv8_consumers_sync();  // the other parity has been read
+        if (!one) kv8_consumers_sync();    // what the buffer held has been read
         if (direct || upper) put();
         kv8_consumers_sync();
         if (!direct) {
@@ -773,8 +857,8 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
         auto join = [&](auto slots, auto stride) {
             constexpr int SLOTS = decltype(slots)::value, STEP = decltype(stride)::value;
             const int n_heads = (p.G + 1 - e) / 2;              // heads 2 y + e
-            for (int x = (int)threadIdx.x; x < n_heads * (D / 4); x += 256) {
-                const int y = x / (D / 4), d4 = x % (D / 4);
+            for (int x = reader; x < n_heads * (D / 4); x += 256) {
+                const int head = x / (D / 4), d4 = x % (D / 4), y = first + head;
                 float mk[SLOTS], M = -INFINITY, L = 0.f;
 #pragma unroll
                 for (int k = 0; k < SLOTS; ++k) {
@@ -794,25 +878,13 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
                     O.z = fmaf(b.x, f, O.z);
                     O.w = fmaf(b.y, f, O.w);
                 }
-                emit(2 * y + e, d4, O, M, L);
+                emit(2 * head + e, d4, O, M, L);
             }
         };
-        if (direct) join(std::integral_constant<int, C::CONSUMERS>{}, std::integral_constant<int, 2>{});
+        if (one) join(std::integral_constant<int, C::CONSUMERS>{}, std::integral_constant<int, 1>{});
+        else if (direct) join(std::integral_constant<int, C::CONSUMERS>{}, std::integral_constant<int, 2>{});
         else join(std::integral_constant<int, C::KSLOTS / 2>{}, std::integral_constant<int, NRG * HH>{});
     }
-}
-
-// Place of four features (from f, a multiple of 4) of query head h among the products' B operands: groups of eight
-// heads, steps, lanes; the features are taken in the order of a key row's bytes in kv8_tile.
-template <int D>
-__device__ __forceinline__ int kv8_q_place(int h, int f) {
-    constexpr int PER = D / 4;                                  // features of a lane (t)
-    const int st = (f % PER) / 4;
-    return (((h >> 3) * (D / 32) + st / 2) * 32 + (h & 7) * 4 + f / PER) * 2 + (st & 1);
-}
-__device__ __forceinline__ uint2 bf16x4_to_half4(uint2 raw) {
-    return make_uint2(pack_half2(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u)),
-                      pack_half2(__uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)));
 }
 
 // tm_k, tm_v: the caches as {D, n_pages * Hkv * P} bytes.
@@ -823,9 +895,9 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
     using C = Kv8AttnCfg<D, NT, NRG>;
     extern __shared__ __align__(1024) uint8_t dsmem[];
     const Kv8Shared<C> sh(dsmem);
-    __shared__ int s_warp_sum[C::CONSUMERS + 1];
+    __shared__ int s_warp_sum[C::CONSUMERS + C::SETS];
     __shared__ int s_from[6], s_to, s_last;
-    __shared__ volatile int s_walk[2][8], s_units[2];
+    __shared__ volatile int s_walk[C::CONSUMERS][8], s_units[2];
 
     const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31u);
     // this block's units: chunks before each request, summed over a slice of the requests per thread
@@ -852,7 +924,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
     __syncthreads();
     int total = 0;
 #pragma unroll
-    for (int i = 0; i <= C::CONSUMERS; ++i) {
+    for (int i = 0; i < C::CONSUMERS + C::SETS; ++i) {
         if (i == warp) incl += total;
         total += s_warp_sum[i];
     }
@@ -901,36 +973,34 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
     w.set(s_from[4], s_from[5]);
     if (u0 == w.begin + w.size()) w.next(p);
 
-    if (warp == C::CONSUMERS) {
-        kv8_produce<D, C, false>(tm_k, tm_v, p, sh, w, u0, u1, lane, false);
+    if (warp >= C::CONSUMERS) {
+        kv8_produce<D, C, false>(tm_k, tm_v, p, sh, w, u0, u1, warp - C::CONSUMERS, lane, false);
         return;
     }
     grid_dependency_wait();
     const int set = warp / NRG / kKv8Tiles % C::SETS;
-    Kv8Place at_ring{0, set, set, 0u, true};
-    int turn = 0;
-    for (int u = u0; u < s_to; turn ^= 1) {
+    Kv8Place at_ring{set, set, 0u, true};
+    const int q_log = Kv8Shared<C>::q_ring_log(p.G * D / 8);
+    volatile int* at = s_walk[warp];
+    int turn = 0;                                          // pieces
+    for (int u = u0; u < s_to;) {
         const int end = min(s_to, w.begin + w.nch);    // of its units with keys
-        for (int x = (int)threadIdx.x; x < C::NTG * 8 * (D / 4); x += 256) {
-            const int h = x / (D / 4), f = 4 * (x % (D / 4));
-            uint2 raw = make_uint2(0u, 0u);
-            if (h < p.G)
-                raw = *reinterpret_cast<const uint2*>(p.qh + ((long long)w.b * p.H + (long long)w.hk * p.G + h) * D + f);
-            sh.q[kv8_q_place<D>(h, f)] = bf16x4_to_half4(raw);
-        }
-        // The walk goes through shared memory over the loop on the keys, which needs every register; in turn, so that a
-        // warp that is behind still finds its piece's.
-        volatile int* at = s_walk[turn];
-        if (threadIdx.x == 0) {
+        // the walk goes through shared memory over the loop on the keys, which needs every register
+        __syncwarp();
+        if (lane == 0) {
             at[0] = w.b;
             at[1] = w.hk;
             at[2] = w.begin;
             at[3] = end;
             at[4] = u == w.begin && end == w.begin + w.nch;            // the item is this block's alone
             at[5] = 2 * (int)blockIdx.x + (r0 < w.begin ? 1 : 0);      // else: the piece's place
+            at[6] = turn;
         }
-        kv8_consumers_sync();              // and the last piece's results have been read
-        kv8_piece<D, NT, NRG, C>(p, sh, w, w.ch0 + (u - w.begin), w.ch0 + (end - w.begin), at_ring, warp, lane,
+        __syncwarp();
+        if (at_ring.ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(sh.q_full + (turn & ((1 << q_log) - 1))), (uint32_t)(turn >> q_log) & 1u,
+                                                             p.wait_limit_ns, kSiteKv8Full)))
+            at_ring.ok = false;
+        kv8_piece<D, NT, NRG, C>(p, sh, w, w.ch0 + (u - w.begin), w.ch0 + (end - w.begin), at_ring, at + 6, q_log, warp, lane,
                                  [&](int h, int d4, const float4& O, float M, float L) {
                                      if (at[4]) {
                                          kv8_store4<D>(p, at[0], at[1], h, d4, O, M, L);
@@ -940,6 +1010,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
                                          if (d4 == 0) *reinterpret_cast<float2*>(pt + D) = make_float2(M, L);
                                      }
                                  });
+        turn = at[6] + 1;
         w.b = at[0];
         w.hk = at[1];
         w.begin = at[2];
@@ -1055,6 +1126,7 @@ __global__ void __launch_bounds__(Kv8StepCfg<D>::THREADS, 2)
     __shared__ float4 s_tab32[HALF];
     __shared__ double2 s_tab64[HALF];
     __shared__ __align__(16) float s_part[8 * (D + 4)];        // this block's sums: [head][O, then M and L]
+    __shared__ volatile int s_turn;                            // the only piece's number
     const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31u);
     const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
     const int item = (int)blockIdx.x / ranks;
@@ -1070,13 +1142,16 @@ __global__ void __launch_bounds__(Kv8StepCfg<D>::THREADS, 2)
         }
         return;
     }
-    if (threadIdx.x == 0) sh.init_barriers();
+    if (threadIdx.x == 0) {
+        sh.init_barriers();
+        s_turn = 0;
+    }
     __syncthreads();
     const int share = (w.nch + ranks - 1) / ranks;
     const int u0 = min(w.nch, rank * share), u1 = min(w.nch, u0 + share);
     const bool append = tk.k != nullptr && u0 < u1 && u1 == w.nch;
-    if (warp == C::CONSUMERS) {
-        kv8_produce<D, C, true>(tm_k, tm_v, p, sh, w, u0, u1, lane, append);
+    if (warp >= C::CONSUMERS) {
+        kv8_produce<D, C, true>(tm_k, tm_v, p, sh, w, u0, u1, warp - C::CONSUMERS, lane, append);
     } else {
         const int row = (int)threadIdx.x / TPR, c = (int)threadIdx.x % TPR;
         Kv8Row<D> r;
@@ -1089,17 +1164,17 @@ __global__ void __launch_bounds__(Kv8StepCfg<D>::THREADS, 2)
         if (append) {
             __threadfence();
             asm volatile("fence.proxy.async.global;" ::: "memory");
-            asm volatile("bar.arrive 2, %0;" ::"n"(C::THREADS) : "memory");
+            asm volatile("bar.arrive 2, %0;" ::"n"(32 * (C::CONSUMERS + 1)) : "memory");
         }
-        if (row < 8) {
-            const bool head = row < p.G;
-            sh.q[kv8_q_place<D>(row, 4 * c)] = head ? bf16x4_to_half4(o0) : make_uint2(0u, 0u);
-            sh.q[kv8_q_place<D>(row, HALF + 4 * c)] = head ? bf16x4_to_half4(o1) : make_uint2(0u, 0u);
+        if (row < p.G) {
+            uint2* q = reinterpret_cast<uint2*>(sh.q);
+            q[kv8_q_place<D>(row, 4 * c)] = bf16x4_to_half4(o0);
+            q[kv8_q_place<D>(row, HALF + 4 * c)] = bf16x4_to_half4(o1);
         }
         kv8_consumers_sync();
         const int set = warp / kKv8Tiles % C::SETS;
-        Kv8Place at_ring{0, set, set, 0u, true};
-        kv8_piece<D, 1, 1, C>(p, sh, w, w.ch0 + u0, w.ch0 + u1, at_ring, warp, lane,
+        Kv8Place at_ring{set, set, 0u, true};
+        kv8_piece<D, 1, 1, C>(p, sh, w, w.ch0 + u0, w.ch0 + u1, at_ring, &s_turn, 0, warp, lane,
                               [&](int h, int d4, const float4& O, float M, float L) {
                                   if (ranks == 1) {
                                       kv8_store4<D>(p, w.b, w.hk, h, d4, O, M, L);

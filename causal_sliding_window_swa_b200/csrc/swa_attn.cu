@@ -1510,6 +1510,14 @@ int launch_kv8_decode(int dev, const swa::Kv8AttnParams& a, const swa::Kv8TokenP
         return launch_kv8_step<D>(dev, tk, tv, a, t, ranks, st);
     const int rows_per_block = 256 / (D / 8);
     const dim3 grid((unsigned)a.B, (unsigned)((a.H + (t.k ? a.c.Hkv : 0) + rows_per_block - 1) / rows_per_block));
+    {
+        // the attention kernel's split of L1 and shared memory, so that its blocks start beside these
+        static std::once_flag once[64];
+        std::call_once(once[dev], [&] {
+            cudaFuncSetAttribute(swa::kv8_token_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared);
+        });
+    }
     swa::kv8_token_kernel<D><<<grid, 256, 0, st>>>(t);
     if (a.G <= 8) return launch_kv8_attention_n<D, 1, 1>(dev, tk, tv, a, st);
     if (a.G <= 16) return launch_kv8_attention_n<D, 2, 1>(dev, tk, tv, a, st);
@@ -1561,9 +1569,9 @@ int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void*
     int* counters = reinterpret_cast<int*>(ws + L.counters);
     const swa::Kv8TokenParams t{static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v),
                                 static_cast<const bf*>(ve), static_cast<const bf*>(gate_x), static_cast<const bf*>(Wg),
-                                block_table, seq_len, reinterpret_cast<bf*>(ws + L.qh), static_cast<bf*>(out), lse, c, H,
+                                block_table, seq_len, reinterpret_cast<uint2*>(ws + L.qh), static_cast<bf*>(out), lse, c, H,
                                 max_pages, counters, swa::kv8_max_blocks(H / Hkv), (double)rope_base, (double)eps};
-    const swa::Kv8AttnParams a{reinterpret_cast<const bf*>(ws + L.qh), block_table, seq_len, doc_start, static_cast<bf*>(out),
+    const swa::Kv8AttnParams a{reinterpret_cast<const uint2*>(ws + L.qh), block_table, seq_len, doc_start, static_cast<bf*>(out),
                                lse, c, counters, reinterpret_cast<float*>(ws + L.part), B, H, H / Hkv, max_pages,
                                std::max(0, window), (float)(1.4426950408889634 / std::sqrt((double)D)), wait_limit_ns()};
     return D == 128 ? launch_kv8_decode<128>(dev, a, t, st) : launch_kv8_decode<64>(dev, a, t, st);
