@@ -280,7 +280,8 @@ struct Kv8Cfg {
     static constexpr int CONSUMERS = 8;
     static constexpr int BLOCKS_PER_SM = NT == 1 ? 2 : 1;
     static constexpr int KSLOTS = CONSUMERS / NRG;               // warps that share the keys of a group of heads
-    static constexpr int SETS = KSLOTS / kKv8Tiles;              // chunks in work at a time, each set with a producer warp
+    static constexpr int SETS = KSLOTS > kKv8Tiles ? KSLOTS / kKv8Tiles : 1;    // chunks in work at a time, each with a producer
+    static constexpr int TPW = KSLOTS < kKv8Tiles ? kKv8Tiles / KSLOTS : 1;     // tiles of a chunk for each warp
     static constexpr int THREADS = 32 * (CONSUMERS + SETS);
     static constexpr int TENSOR = kKv8Chunk * D;                 // bytes of a chunk's K (and V)
     static constexpr int HEADS = 8 * NT;                         // query heads of a warp
@@ -771,18 +772,22 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[x][k][e] = 0.f;
     }
-    const int tile = kslot % kKv8Tiles, tile_box = tile >> (min(p.c.log_p, 6) - 4);
-    const int n_chunks = c_end - c_begin, first_pos = c_begin * kKv8Chunk + 16 * tile;
+    const int tile0 = kslot * C::TPW % kKv8Tiles, box_tiles = min(p.c.log_p, 6) - 4;
+    const int n_chunks = c_end - c_begin, first_pos = c_begin * kKv8Chunk + 16 * tile0;
     for (; at_ring.next < n_chunks; at_ring.next += C::SETS) {
         const int s = at_ring.s;
         if (at_ring.ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(sh.full + s), at_ring.phase, p.wait_limit_ns, kSiteKv8Full)))
             at_ring.ok = false;
         if (!at_ring.ok) break;
-        const int pos0 = first_pos + at_ring.next * kKv8Chunk;
-        const float4 meta = sh.meta[s * kKv8Tiles + tile_box];
-        // not wanted: outside the visible keys, or on a page that is not there
-        if (pos0 + 16 > w.lo && pos0 < w.n && meta.y >= 0.f)
-            kv8_tile<D, NT>(sh.ring + (2 * s) * C::TENSOR + tile * 16 * D, C::TENSOR, pos0, w.lo, w.n, meta, q, o, m, l, g, t);
+#pragma unroll
+        for (int k = 0; k < C::TPW; ++k) {
+            const int pos0 = first_pos + at_ring.next * kKv8Chunk + 16 * k;
+            const float4 meta = sh.meta[s * kKv8Tiles + ((tile0 + k) >> box_tiles)];
+            // not wanted: outside the visible keys, or on a page that is not there
+            if (pos0 + 16 > w.lo && pos0 < w.n && meta.y >= 0.f)
+                kv8_tile<D, NT>(sh.ring + (2 * s) * C::TENSOR + (tile0 + k) * 16 * D, C::TENSOR, pos0, w.lo, w.n, meta, q, o, m,
+                                l, g, t);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(sh.empty + s));
         if ((at_ring.s += C::SETS) >= C::NS) {
