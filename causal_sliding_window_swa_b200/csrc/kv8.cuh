@@ -88,11 +88,12 @@ __device__ __forceinline__ uint32_t recode4(uint32_t c, float down) {
 // ------------------------------------------------------------------------------------------- write
 
 // The tokens of one call are consecutive rows; a run is a stretch of them that goes into consecutive
-// slots of one page.  One block per (window of `win` tokens, head) takes the runs that begin in its
-// window: a run of one token by the D/8 lanes of a row group, a longer one by the whole block, its
+// slots of one page.  A group of W warps per (window of `win` tokens, head) takes the runs that begin in its
+// window: a run of one token by the D/8 lanes of a row, a longer one by the whole group, its
 // rows kept in registers between the maximum and the encoding, so that khat and v' are read once.
-// HBM-bound on prompts, where most windows are one page: the window's rows are loaded before its slots are
-// known, and used where a run begins with the window.
+// HBM-bound on prompts, where windows are pages long: the first slot says where the window's next page
+// begins, and the rows from there on are loaded before the other slots are looked at.  W gives each thread
+// four rows of a page (eight of the largest): with fewer, small pages leave too little in flight.
 struct Kv8Store {
     uint8_t* k_cache;
     uint8_t* v_cache;
@@ -110,20 +111,26 @@ __device__ __forceinline__ void recode_rows(uint8_t* block, int rows, float down
     }
 }
 
-template <int D, int IT>
-__global__ void __launch_bounds__(256) kv8_write_kernel(const __nv_bfloat16* __restrict__ kh,
+template <int D, int W, int IT>
+__global__ void __launch_bounds__(256, IT == 4 ? 4 : 2) kv8_write_kernel(const __nv_bfloat16* __restrict__ kh,
                                                         const __nv_bfloat16* __restrict__ vp,
                                                         const int* __restrict__ slots, const Kv8Store c, int n_tokens,
-                                                        int win) {
-    constexpr int TPR = D / 8, RPB = 256 / TPR;
+                                                        int row_tokens, int win, int windows) {
+    constexpr int TPR = D / 8, THREADS = 32 * W, GROUPS = 8 / W, RPG = THREADS / TPR;
     const int P = 1 << c.log_p;
     const int h = (int)blockIdx.y;
-    const long long t0 = (long long)blockIdx.x * win;
-    const int group = (int)threadIdx.x / TPR, l8 = (int)threadIdx.x % TPR;
-    const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+    const int grp = (int)threadIdx.x / THREADS, tid = (int)threadIdx.x % THREADS;
+    // rows of row_tokens tokens, each of `windows` windows
+    const int window = (int)blockIdx.x * GROUPS + grp, row = window / windows, in_row = window - row * windows;
+    const long long t0 = (long long)row * row_tokens + (long long)in_row * win;
+    if (t0 >= n_tokens) return;
+    const int group = tid / TPR, l8 = tid % TPR;
+    const int lane = tid & 31, warp = tid >> 5;
     const int n_slots = c.n_pages << c.log_p;
-    __shared__ int s_run[128], s_n, s_len, s_single;
-    __shared__ uint32_t s_max[2][8];
+    __shared__ int s_runs[128], s_n[GROUPS], s_len[GROUPS], s_single[GROUPS];     // GROUPS * P <= 128
+    __shared__ uint32_t s_max[GROUPS][2][W];
+    int* s_run = s_runs + grp * P;
+    auto sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(THREADS) : "memory"); };
 
     auto slot_at = [&](long long t) -> int { return t < n_tokens ? __ldg(slots + t) : -1; };
     // token t goes on where token t - 1 ended
@@ -140,7 +147,7 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(const __nv_bfloat16* __r
     auto load_rows = [&](long long t, int len) {
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
-            const int r = group + it * RPB;
+            const int r = group + it * RPG;
             if (r < len) {
                 const long long at = ((t + r) * c.Hkv + h) * D + 8 * l8;
                 x[0][it] = ldg_stream16(kh + at);
@@ -161,80 +168,79 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(const __nv_bfloat16* __r
             uint32_t m = 0u;
 #pragma unroll
             for (int it = 0; it < IT; ++it)
-                if (group + it * RPB < len)
+                if (group + it * RPG < len)
                     m = max_abs2(max_abs2(max_abs2(max_abs2(m, x[u][it].x), x[u][it].y), x[u][it].z), x[u][it].w);
             uint32_t a = max_half(m);
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
-            if (lane == 0) s_max[u][warp] = a;
+            if (lane == 0) s_max[grp][u][warp] = a;
         }
-        __syncthreads();                   // (and every thread has read the old scales)
+        sync();                   // (and every thread has read the old scales)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            uint32_t a = s_max[u][0];
+            uint32_t a = s_max[grp][u][0];
 #pragma unroll
-            for (int w = 1; w < 8; ++w) a = max(a, s_max[u][w]);
+            for (int w = 1; w < W; ++w) a = max(a, s_max[grp][u][w]);
             int e = scale_exponent(a);
             uint8_t* blk = block_of(u == 0 ? c.k_cache : c.v_cache, slot);
             if (off > 0) {
-                if (e > old[u]) recode_rows<D>(blk, off, scale_of(max(old[u] - e, -126)), group, RPB, l8);
+                if (e > old[u]) recode_rows<D>(blk, off, scale_of(max(old[u] - e, -126)), group, RPG, l8);
                 e = max(e, old[u]);
             }
             const float inv = scale_of(-e);
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
-                const int r = group + it * RPB;
+                const int r = group + it * RPG;
                 if (r < len)
                     *reinterpret_cast<uint2*>(blk + (long long)(off + r) * D + 8 * l8) =
                         make_uint2(encode4(x[u][it].x, x[u][it].y, inv), encode4(x[u][it].z, x[u][it].w, inv));
             }
-            if (threadIdx.x == 0) *sc[u] = scale_of(e);
+            if (tid == 0) *sc[u] = scale_of(e);
         }
-        __syncthreads();
+        sync();
     };
 
-    const int here = (int)min((long long)win, n_tokens - t0);      // tokens of the window
-    if (win >= P) load_rows(t0, min(here, P));
-    if (threadIdx.x == 0) {
-        s_n = 0;
-        s_len = P;
-        s_single = 0;
+    const int here = min(win, row_tokens - in_row * win);          // tokens of the window
+    // the page that begins in the window, where its tokens are consecutive: at token `next`
+    const int slot0 = slot_at(t0), next = win == P && slot0 >= 0 ? -slot0 & (P - 1) : here;
+    if (next < here) load_rows(t0 + next, (int)min((long long)P, n_tokens - t0 - next));
+    if (tid == 0) {
+        s_n[grp] = 0;
+        s_len[grp] = P;
+        s_single[grp] = 0;
     }
-    __syncthreads();
-    const int slot0 = slot_at(t0);
-    if ((int)threadIdx.x < win) {
-        const long long t = t0 + threadIdx.x;
+    sync();
+    const int slot1 = next < here ? slot_at(t0 + next) : -1;
+    const bool whole = slot1 >= 0 && slot1 < n_slots && !goes_on(t0 + next);      // a run begins there
+    if (tid < here) {
+        const long long t = t0 + tid;
         const int s = slot_at(t);
         if (s >= n_slots) record_error(kErrIndex, kSiteKvSlot);
-        const bool on = goes_on(t), next_on = goes_on(t + 1);
-        if (s >= 0 && s < n_slots && !on) {
-            if (!next_on) s_single = 1;
-            else if (threadIdx.x > 0 || win < P) s_run[atomicAdd(&s_n, 1)] = (int)threadIdx.x;
+        if (s >= 0 && s < n_slots && !goes_on(t)) {
+            if (!goes_on(t + 1)) s_single[grp] = 1;
+            else if (tid != next) s_run[atomicAdd(&s_n[grp], 1)] = tid;
         }
-        if (threadIdx.x > 0 && threadIdx.x < P && !on) atomicMin(&s_len, (int)threadIdx.x);
     }
-    __syncthreads();
-    // the run that begins with the window: it ends within it, or at the page's end
-    if (win >= P && slot0 >= 0 && slot0 < n_slots && !goes_on(t0)) {
-        const int len = min(s_len, here);
-        if (len > 1) store_run(slot0, len);
-    }
-    const int n_runs = s_n;
+    if (whole && tid > 0 && tid < P && !goes_on(t0 + next + tid)) atomicMin(&s_len[grp], tid);
+    sync();
+    if (whole && s_len[grp] > 1) store_run(slot1, s_len[grp]);
+    const int n_runs = s_n[grp];
     for (int i = 0; i < n_runs; ++i) {
         const long long t = t0 + s_run[i];
-        if (threadIdx.x == 0) s_len = P;
-        __syncthreads();
-        if (threadIdx.x >= 1 && (int)threadIdx.x < P && !goes_on(t + threadIdx.x)) atomicMin(&s_len, (int)threadIdx.x);
-        __syncthreads();
-        const int len = s_len;
+        sync();                            // the length before it has been read
+        if (tid == 0) s_len[grp] = P;
+        sync();
+        if (tid >= 1 && tid < P && !goes_on(t + tid)) atomicMin(&s_len[grp], tid);
+        sync();
+        const int len = s_len[grp];
         load_rows(t, len);
         store_run(slot_at(t), len);
     }
     // runs of one token
-    if (s_single == 0) return;
-    for (int g0 = 0; g0 < win; g0 += RPB) {
+    if (s_single[grp] == 0) return;
+    for (int g0 = 0; g0 < here; g0 += RPG) {
         const long long t = t0 + g0 + group;
-        const int slot = g0 + group < win ? slot_at(t) : -1;
+        const int slot = g0 + group < here ? slot_at(t) : -1;
         const bool mine = slot >= 0 && slot < n_slots && !goes_on(t) && !goes_on(t + 1);
         const int off = slot & (P - 1), page = slot >> c.log_p;
 #pragma unroll
@@ -268,24 +274,23 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(const __nv_bfloat16* __r
 
 // -------------------------------------------------------------------------------------------- read
 
-// Row r = token * Hkv + h of the results: D/8 lanes, 8 features each; a thread has kReadRows rows in flight.  Slots
+// Row r = token * Hkv + h of the results: D/8 lanes, 8 features each; a thread has NR rows in flight.  Slots
 // below 0 (and past the cache, which is recorded) give zero rows.
-constexpr int kReadRows = 2;
 __device__ __forceinline__ uint2 decode4(uint32_t c, float s) {
     const float2 a = decode2(c), b = decode2(c >> 16);
     return make_uint2(pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(b.x * s, b.y * s));
 }
-template <int D>
+template <int D, int NR>
 __global__ void __launch_bounds__(256) kv8_read_kernel(const int* __restrict__ slots, const Kv8Store c,
                                                        __nv_bfloat16* __restrict__ kh, __nv_bfloat16* __restrict__ vp,
                                                        int n_rows, FastDiv divH) {
     constexpr int TPR = D / 8, STEP = 256 / TPR;
     const int l8 = 8 * ((int)threadIdx.x % TPR);
     const int n_slots = c.n_pages << c.log_p;
-    const long long r0 = (long long)blockIdx.x * STEP * kReadRows + (int)threadIdx.x / TPR;
-    int slot[kReadRows], h[kReadRows];
+    const long long r0 = (long long)blockIdx.x * STEP * NR + (int)threadIdx.x / TPR;
+    int slot[NR], h[NR];
 #pragma unroll
-    for (int x = 0; x < kReadRows; ++x) {
+    for (int x = 0; x < NR; ++x) {
         const long long r = r0 + x * STEP;
         slot[x] = -1;
         if (r < n_rows) {
@@ -298,10 +303,10 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const int* __restrict__ s
             }
         }
     }
-    uint2 w[kReadRows][2];
-    float s[kReadRows][2];
+    uint2 w[NR][2];
+    float s[NR][2];
 #pragma unroll
-    for (int x = 0; x < kReadRows; ++x) {
+    for (int x = 0; x < NR; ++x) {
         w[x][0] = w[x][1] = make_uint2(0u, 0u);
         s[x][0] = s[x][1] = 0.f;
         if (slot[x] < 0) continue;
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const int* __restrict__ s
         s[x][1] = c.v_scale[ph];
     }
 #pragma unroll
-    for (int x = 0; x < kReadRows; ++x) {
+    for (int x = 0; x < NR; ++x) {
         const long long r = r0 + x * STEP;
         if (r >= n_rows) continue;
 #pragma unroll

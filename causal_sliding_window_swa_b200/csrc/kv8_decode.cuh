@@ -251,10 +251,11 @@ constexpr int kKv8Tiles = kKv8Chunk / 16;
 constexpr int kKv8Sms = 148;
 // Blocks of the attention kernel, at most: two per SM where a warp has one group of eight heads, else one.
 __host__ __device__ constexpr int kv8_max_blocks(int G) { return G <= 8 ? 2 * kKv8Sms : kKv8Sms; }
-constexpr int kKv8ItemCost = 2;         // what an item costs beside its units, in units (sharing out the work)
-constexpr int kKv8MinShare = 6;         // units of a block, where there are few
-constexpr int kKv8StepChunks = 8;       // chunks of a block in the one-launch form, at most
-constexpr int kKv8Whole = 4;            // items of at most so many units are not split
+constexpr int kKv8ItemCost = 4;         // what an item costs beside its units, in units (sharing out the work)
+constexpr int kKv8StepChunks = 48;      // chunks of a block in the one-launch form, at most
+// Units of a block, where there are few.
+__host__ __device__ constexpr int kv8_min_share(int G) { return G <= 8 ? 2 : 6; }
+constexpr int kKv8Whole = 16;           // items of at most so many units are not split
 constexpr float kSlack = 10.f;          // fp16 holds 2^15
 
 enum : unsigned int { kSiteKv8Full = 83, kSiteKv8Empty = 84 };
@@ -934,8 +935,11 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
         total += s_warp_sum[i];
     }
     const int n_units = total * p.c.Hkv;
-    const int n_blocks = min((int)gridDim.x, (n_units + kKv8MinShare - 1) / kKv8MinShare);
-    if ((int)blockIdx.x >= n_blocks) return;
+    const int n_blocks = min((int)gridDim.x, (n_units + kv8_min_share(p.G) - 1) / kv8_min_share(p.G));
+    if ((int)blockIdx.x >= n_blocks) {
+        grid_dependency_wait();        // this grid does not end before the token kernel, even where it has no units
+        return;
+    }
     if (threadIdx.x == 0) {
         s_units[0] = n_units;
         s_units[1] = n_blocks;

@@ -1291,12 +1291,30 @@ int check_kv8_rows(int B, int T, int Hkv, int D, const void* kh, const void* vp,
     return SWA_OK;
 }
 
-template <int D, int IT>
-void launch_kv8_write(const void* kh, const void* vp, const int* slots, const swa::Kv8Store& c, int n_tokens, int win,
+// Two rows to a thread, one where all blocks of that run at once (7 x 333 tokens of 6 heads: 2.1 us against 2.6; 32768
+// tokens of 12 heads: 45 us by two, 52 by one).
+template <int D>
+void launch_kv8_read(int dev, const int* slots, const swa::Kv8Store& c, __nv_bfloat16* kh, __nv_bfloat16* vp, int n_rows,
+                     const swa::FastDiv& divH, cudaStream_t st) {
+    constexpr int ROWS = 256 / (D / 8);
+    const unsigned blocks = ((unsigned)n_rows + ROWS - 1) / ROWS;
+    if (blocks <= 8u * (unsigned)g_num_sms[dev])
+        swa::kv8_read_kernel<D, 1><<<blocks, 256, 0, st>>>(slots, c, kh, vp, n_rows, divH);
+    else
+        swa::kv8_read_kernel<D, 2><<<(blocks + 1) / 2, 256, 0, st>>>(slots, c, kh, vp, n_rows, divH);
+}
+
+// Windows are pages of a row's tokens; rows of one token share windows, a token to each of a group's rows of lanes
+// (1024 x 1 tokens of 12 heads: 8 us, against 62 with a window each).
+template <int D, int W, int IT>
+void launch_kv8_write(const void* kh, const void* vp, const int* slots, const swa::Kv8Store& c, int B, int T,
                       cudaStream_t st) {
-    const dim3 grid((unsigned)((n_tokens + (long long)win - 1) / win), (unsigned)c.Hkv);
-    swa::kv8_write_kernel<D, IT><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(kh),
-                                                       static_cast<const __nv_bfloat16*>(vp), slots, c, n_tokens, win);
+    const int win = T > 1 ? 1 << c.log_p : 32 * W / (D / 8), row_tokens = T > 1 ? T : B, rows = T > 1 ? B : 1;
+    const int windows = (row_tokens - 1) / win + 1;
+    const dim3 grid((unsigned)(((long long)windows * rows * W + 7) / 8), (unsigned)c.Hkv);
+    swa::kv8_write_kernel<D, W, IT><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(kh),
+                                                          static_cast<const __nv_bfloat16*>(vp), slots, c, B * T,
+                                                          row_tokens, win, windows);
 }
 
 }  // namespace
@@ -1330,7 +1348,7 @@ int swa_attn_kv_pages(const int* block_table, const int* kv_len, const int* firs
                        pool_out, slots, step_len, B, T, max_pages, n_pages, log_p, std::max(0, window)};
     cudaLaunchConfig_t cfg = {};
     // one block for small steps, a cluster of eight for more table entries and slots
-    const unsigned ranks = (long long)B * ((long long)max_pages + T) <= 4096 ? 1u : 8u;
+    const unsigned ranks = (long long)B * ((long long)max_pages + T) <= 2048 ? 1u : 8u;
     cfg.gridDim = dim3(ranks);
     cfg.blockDim = dim3(1024);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
@@ -1359,21 +1377,17 @@ int swa_attn_kv8_write(const void* kh, const void* vp, const int* slots, void* k
     if ((rc = device_ready(&dev)) != SWA_OK) return rc;
     const swa::Kv8Store c{static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale, v_scale, n_pages, Hkv,
                           log_p};
-    const int n_tokens = B * T;
-    const int rows = 256 / (D / 8);
-    // windows of one page; smaller ones while they do not fill the GPU
-    const int win = (long long)(n_tokens / rows) * Hkv <= 8ll * g_num_sms[dev] ? rows : std::max(rows, page_size);
-    const int it = std::max(1, page_size / rows);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (D == 128) {
-        if (it == 1) launch_kv8_write<128, 1>(kh, vp, slots, c, n_tokens, win, st);
-        else if (it == 2) launch_kv8_write<128, 2>(kh, vp, slots, c, n_tokens, win, st);
-        else if (it == 4) launch_kv8_write<128, 4>(kh, vp, slots, c, n_tokens, win, st);
-        else launch_kv8_write<128, 8>(kh, vp, slots, c, n_tokens, win, st);
+        if (page_size == 16) launch_kv8_write<128, 2, 4>(kh, vp, slots, c, B, T, st);
+        else if (page_size == 32) launch_kv8_write<128, 4, 4>(kh, vp, slots, c, B, T, st);
+        else if (page_size == 64) launch_kv8_write<128, 8, 4>(kh, vp, slots, c, B, T, st);
+        else launch_kv8_write<128, 8, 8>(kh, vp, slots, c, B, T, st);
     } else {
-        if (it == 1) launch_kv8_write<64, 1>(kh, vp, slots, c, n_tokens, win, st);
-        else if (it == 2) launch_kv8_write<64, 2>(kh, vp, slots, c, n_tokens, win, st);
-        else launch_kv8_write<64, 4>(kh, vp, slots, c, n_tokens, win, st);
+        if (page_size == 16) launch_kv8_write<64, 1, 4>(kh, vp, slots, c, B, T, st);
+        else if (page_size == 32) launch_kv8_write<64, 2, 4>(kh, vp, slots, c, B, T, st);
+        else if (page_size == 64) launch_kv8_write<64, 4, 4>(kh, vp, slots, c, B, T, st);
+        else launch_kv8_write<64, 8, 4>(kh, vp, slots, c, B, T, st);
     }
     return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
@@ -1391,15 +1405,11 @@ int swa_attn_kv8_read(const int* slots, const void* k_cache, const void* v_cache
     const swa::Kv8Store c{static_cast<uint8_t*>(const_cast<void*>(k_cache)), static_cast<uint8_t*>(const_cast<void*>(v_cache)),
                           const_cast<float*>(k_scale), const_cast<float*>(v_scale), n_pages, Hkv, log_p};
     const int n_rows = B * T * Hkv;
-    const int rows_per_block = 256 / (D / 8) * swa::kReadRows;
-    const long long blocks = ((long long)n_rows + rows_per_block - 1) / rows_per_block;
     const swa::FastDiv divH = make_fastdiv(Hkv);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     __nv_bfloat16 *kp = static_cast<__nv_bfloat16*>(kh), *vpp = static_cast<__nv_bfloat16*>(vp);
-    if (D == 128)
-        swa::kv8_read_kernel<128><<<(unsigned)blocks, 256, 0, st>>>(slots, c, kp, vpp, n_rows, divH);
-    else
-        swa::kv8_read_kernel<64><<<(unsigned)blocks, 256, 0, st>>>(slots, c, kp, vpp, n_rows, divH);
+    if (D == 128) launch_kv8_read<128>(dev, slots, c, kp, vpp, n_rows, divH, st);
+    else launch_kv8_read<64>(dev, slots, c, kp, vpp, n_rows, divH, st);
     return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
@@ -1460,33 +1470,57 @@ int launch_kv8_attention_n(int dev, const CUtensorMap& tk, const CUtensorMap& tv
     return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
-// The step as one launch (kv8_step_kernel), clusters of `ranks` blocks.
+// The step as one launch (kv8_step_kernel): what its launches need, once per device.
+template <int D>
+struct Kv8StepLaunch {
+    bool ok = false;
+    int clusters[swa::kDecodeMaxCluster + 1] = {0};    // of so many blocks that the GPU holds at a time
+
+    static cudaLaunchConfig_t config(cudaLaunchAttribute* attr, int items, int ranks, cudaStream_t st) {
+        using C = swa::Kv8StepCfg<D>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(items * ranks));
+        cfg.blockDim = dim3(C::THREADS);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cfg.stream = st;
+        attr->id = cudaLaunchAttributeClusterDimension;
+        attr->val.clusterDim.x = (unsigned)ranks;
+        attr->val.clusterDim.y = 1;
+        attr->val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cfg;
+    }
+    static const Kv8StepLaunch& of(int dev) {
+        static std::once_flag once[64];
+        static Kv8StepLaunch all[64];
+        Kv8StepLaunch& l = all[dev];
+        std::call_once(once[dev], [&] {
+            l.ok = cudaFuncSetAttribute(swa::kv8_step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        swa::Kv8StepCfg<D>::SMEM) == cudaSuccess;
+            for (int r = 1; r <= swa::kDecodeMaxCluster && l.ok; ++r) {
+                cudaLaunchAttribute attr;
+                const cudaLaunchConfig_t cfg = config(&attr, 1, r, nullptr);
+                l.ok = cudaOccupancyMaxActiveClusters(&l.clusters[r], swa::kv8_step_kernel<D>, &cfg) == cudaSuccess;
+            }
+            if (!l.ok) cudaGetLastError();
+        });
+        return l;
+    }
+    // The largest cluster of which the GPU holds `items` at a time, 0 where it holds no `items` blocks.  A second wave of
+    // clusters costs a whole step: 48 items of 2048 tokens take 19.4 us by clusters of six (288 blocks), which do not all fit.
+    int ranks(long long items) const {
+        int r = swa::kDecodeMaxCluster;
+        while (r > 0 && clusters[r] < items) --r;
+        return r;
+    }
+};
+
 template <int D>
 int launch_kv8_step(int dev, const CUtensorMap& tk, const CUtensorMap& tv, const swa::Kv8AttnParams& a,
                     const swa::Kv8TokenParams& t, int ranks, cudaStream_t st) {
-    using C = swa::Kv8StepCfg<D>;
-    static std::once_flag once[64];
-    static bool ok[64] = {false};
-    std::call_once(once[dev], [&] {
-        ok[dev] = cudaFuncSetAttribute(swa::kv8_step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) ==
-                  cudaSuccess;
-    });
-    if (!ok[dev]) {
-        cudaGetLastError();
-        return SWA_ERR_CUDA;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.B * a.c.Hkv * ranks));
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ranks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = Kv8StepLaunch<D>::config(&attr, a.B * a.c.Hkv, ranks, st);
     if (cudaLaunchKernelEx(&cfg, swa::kv8_step_kernel<D>, tk, tv, a, t) != cudaSuccess) {
         cudaGetLastError();
         return SWA_ERR_CUDA;
@@ -1500,14 +1534,22 @@ int launch_kv8_decode(int dev, const swa::Kv8AttnParams& a, const swa::Kv8TokenP
     const long long rows = ((long long)a.c.n_pages * a.c.Hkv) << a.c.log_p;
     const int box = std::min(1 << a.c.log_p, swa::kKv8Chunk);
     if (!make_page_map(&tk, a.c.k_cache, rows, D, box) || !make_page_map(&tv, a.c.v_cache, rows, D, box)) return SWA_ERR_CUDA;
-    // One launch where pages do not pass a chunk, every item gets at least one of the resident blocks and the longest possible item leaves a
-    // block no more than kKv8StepChunks chunks.
-    const long long items = (long long)a.B * a.c.Hkv, slots = 2ll * std::min(g_num_sms[dev], swa::kKv8Sms);
+    // One launch where pages do not pass a chunk and the GPU holds a cluster for every item: the largest that it does.  Its
+    // blocks take whole items, so it has to be weighed against the two kernels, which share the chunks out evenly.  With c
+    // chunks for a block (of the longest possible item) and e for an even share, one launch takes about 8.3 + 0.37 c us
+    // and two take 12.3 + 0.63 e: 156 items of 2040 tokens (c 33, e 17) 20.2 against 23.5, 12 of 16380 (33, 11) 21.2 against
+    // 19.3.  No more than kKv8StepChunks, since the lengths may be far from equal.
+    const long long items = (long long)a.B * a.c.Hkv;
     const long long most = (long long)a.max_pages << a.c.log_p;
     const long long chunks = std::min<long long>(most, a.W > 0 ? a.W : most) / swa::kKv8Chunk + 1;
-    const int ranks = (int)std::min<long long>(std::min<long long>(slots / std::max(1ll, items), swa::kDecodeMaxCluster), chunks);
-    if (a.G <= 8 && a.c.log_p <= 6 && ranks >= 1 && (chunks + ranks - 1) / ranks <= swa::kKv8StepChunks)
-        return launch_kv8_step<D>(dev, tk, tv, a, t, ranks, st);
+    if (a.G <= 8 && a.c.log_p <= 6) {
+        const Kv8StepLaunch<D>& step = Kv8StepLaunch<D>::of(dev);
+        if (!step.ok) return SWA_ERR_CUDA;
+        const int ranks = (int)std::min<long long>(step.ranks(items), chunks);
+        const long long share = ranks > 0 ? (chunks + ranks - 1) / ranks : 0, even = items * chunks / (2 * swa::kKv8Sms);
+        if (ranks > 0 && share <= std::min<long long>(swa::kKv8StepChunks, 10 + 3 * even / 2))
+            return launch_kv8_step<D>(dev, tk, tv, a, t, ranks, st);
+    }
     const int rows_per_block = 256 / (D / 8);
     const dim3 grid((unsigned)a.B, (unsigned)((a.H + (t.k ? a.c.Hkv : 0) + rows_per_block - 1) / rows_per_block));
     {
