@@ -369,6 +369,40 @@ struct PageRecord {
 
 constexpr int kPagesSegment = 128;         // entries of a table row, or slots, that a warp has at a time
 
+// A row that changes little, in place, by one thread: at most kPagesFew pages either way, and T <= kPagesFew.
+constexpr int kPagesFew = 4;
+__device__ __forceinline__ bool pages_few(const PageRecord& r) { return r.take <= kPagesFew && r.upto - r.from <= kPagesFew; }
+__device__ __forceinline__ void pages_fill_few(const PagesParams& p, const PageRecord& r, int b) {
+    int* row = p.table_out + (long long)b * p.max_pages;
+    const int P = 1 << p.log_p;
+    const int at = r.L >> p.log_p, partial = r.n > 0 && at < r.have ? row[at] : -1;      // a partly filled page
+    int back[kPagesFew], got[kPagesFew];
+#pragma unroll
+    for (int k = 0; k < kPagesFew; ++k) {
+        if (k < r.upto - r.from) back[k] = row[r.from + k];
+        if (k < r.take) got[k] = p.ring[((unsigned)r.ring_take + (unsigned)k) % (unsigned)p.n_pages];
+    }
+#pragma unroll
+    for (int k = 0; k < kPagesFew; ++k) {
+        if (k < r.upto - r.from) {
+            p.ring[((unsigned)r.ring_give + (unsigned)k) % (unsigned)p.n_pages] = back[k];
+            row[r.from + k] = -1;
+        }
+        if (k < r.take) row[r.have + k] = got[k];
+        if (k < p.T) {
+            int page = -1;
+            if (k < r.n) {
+                const int x = ((r.L + k) >> p.log_p) - r.have;
+                page = partial;
+#pragma unroll
+                for (int y = 0; y < kPagesFew; ++y)
+                    if (x == y) page = got[y];
+            }
+            p.slots[(long long)b * p.T + k] = page >= 0 && page < p.n_pages ? page * P + ((r.L + k) & (P - 1)) : -1;
+        }
+    }
+}
+
 // One segment of row b: entries of the table (seg < table_segs) or slots.
 __device__ __forceinline__ void pages_fill(const PagesParams& p, const PageRecord& r, int b, int seg, int table_segs,
                                            int lane) {
@@ -420,17 +454,16 @@ __device__ __forceinline__ void pages_fill(const PagesParams& p, const PageRecor
     }
 }
 
-// One cluster: every block goes through all requests (1024 at a time) and finds every record, and the blocks share the
-// rows' segments.  A step in place is safe: a block writes a request's state only after every block has read it, and a row's
+// Every block goes through all requests (1024 at a time) and finds every record, and the blocks share the rows'
+// segments.  In place, the blocks are one cluster: a request's state is written only after every block has read it; a row's
 // segments neither read nor write what another one of them changes (the slots read the table entry of a
 // partly filled page, which a step leaves alone; pages are taken from the free stretch of the ring and go back outside it).
-// Latency-bound (the sums, then a table or ring entry, then the stores): one block where all rows are small, else eight.
 __global__ void __launch_bounds__(1024, 1) kv_pages_kernel(const PagesParams p) {
     __shared__ PageRecord s_rec[1024];
     __shared__ int s_warp[2][32];
     __shared__ int s_taken;
     const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
-    const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
+    const int rank = (int)blockIdx.x, ranks = (int)gridDim.x;
     const int P = 1 << p.log_p;
     const int head = min(max(p.pool[0], 0), p.n_pages - 1), free = min(max(p.pool[1], 0), p.n_pages);
     const int table_segs = (p.max_pages + kPagesSegment - 1) / kPagesSegment;
@@ -499,7 +532,7 @@ __global__ void __launch_bounds__(1024, 1) kv_pages_kernel(const PagesParams p) 
         // the sums only grow: the last served request that takes pages has the largest of theirs
         const unsigned takers = __ballot_sync(0xffffffffu, r.take > 0);
         if (takers != 0u && lane == 31 - __clz(takers)) atomicMax(&s_taken, v[0]);
-        if (ranks > 1) cluster_sync_all();
+        if (cluster_nctarank() > 1) cluster_sync_all();
         else __syncthreads();
         if (rank == 0 && b < p.B) {
             const int after = ended ? 0 : r.L + r.n;
@@ -507,9 +540,15 @@ __global__ void __launch_bounds__(1024, 1) kv_pages_kernel(const PagesParams p) 
             p.first_out[b] = ended ? 0 : r.upto;
             p.step_len[b] = ok ? after : 0;
         }
+        const bool few = p.table == p.table_out && p.T <= kPagesFew;
+        if (few) {
+            if (b < p.B && (int)threadIdx.x % ranks == rank && pages_few(r)) pages_fill_few(p, r, b);
+            if (!__syncthreads_or(b < p.B && !pages_few(r))) continue;
+        }
         const int work = min(1024, p.B - b0) * segs;
         for (int x = rank * 32 + warp; x < work; x += ranks * 32) {
             const int row = x / segs;
+            if (few && pages_few(s_rec[row])) continue;
             pages_fill(p, s_rec[row], b0 + row, x - row * segs, table_segs, lane);
         }
         __syncthreads();
