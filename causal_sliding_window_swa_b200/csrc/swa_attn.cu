@@ -1357,11 +1357,11 @@ int swa_attn_kv_pages(const int* block_table, const int* kv_len, const int* firs
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = in_place ? ranks : 1u;
+    attr[0].val.clusterDim.x = ranks;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = in_place && ranks > 1 ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, swa::kv_pages_kernel, p) != cudaSuccess) {
         cudaGetLastError();
         return SWA_ERR_CUDA;

@@ -158,6 +158,37 @@ def test_write_and_read(D, P, Hkv, lens):
     swa.check_device_status()
 
 
+@pytest.mark.parametrize("B,T", [(1, 500), (9, 47), (60, 2), (300, 1), (5, 130)])
+@pytest.mark.parametrize("D,P,Hkv", [(64, 16, 2), (128, 16, 1), (64, 32, 1), (128, 32, 2), (64, 64, 1), (128, 64, 2), (64, 128, 2), (128, 128, 1)])
+def test_write_runs_anywhere(B, T, D, P, Hkv):
+    """Runs of all lengths at all offsets, wherever they lie in a call's rows: between skipped rows, from one request's row into
+    the next one's, several in a page's worth of tokens; three calls into the same pages, each page by one run a call."""
+    r = random.Random(B * T + D + P)
+    g = torch.Generator().manual_seed(P + D)
+    n_pages = B * T // 2 + 4
+    cache = GpuCache(n_pages, Hkv, P, D)
+    fill = [0] * n_pages
+    for _ in range(3):
+        free = r.sample(range(n_pages), n_pages)
+        flat = []
+        while len(flat) < B * T:
+            what = r.choice(["skip", "one", "short", "rest", "rest"])
+            if what == "skip" or not free:
+                flat += [-r.randint(1, 9)] * r.choice([1, 1, 2, r.randint(1, 2 * P)])
+                continue
+            page = free.pop()
+            off = fill[page] if fill[page] < P else 0            # a full page is begun again
+            n = min(P - off, {"one": 1, "short": r.randint(1, 5), "rest": P}[what], B * T - len(flat))
+            flat += range(page * P + off, page * P + off + n)
+            fill[page] = off + n
+        slots = torch.tensor(flat[:B * T], dtype=torch.int32).view(B, T)
+        kh = torch.randn((B, T, Hkv, D), generator=g).to(torch.bfloat16).cuda()
+        vp = (torch.randn((B, T, Hkv, D), generator=g) * torch.exp(2 * torch.randn((B, T, Hkv, 1), generator=g))).to(torch.bfloat16).cuda()
+        cache.write(kh, vp, slots.cuda())
+        cache.check([p * P + i for p, n in enumerate(fill) for i in range(n)])
+    swa.check_device_status()
+
+
 def test_read_rows_written_elsewhere_are_the_same_values():
     # a request that moves: its rows as bf16, into other pages of another page size
     g = torch.Generator().manual_seed(5)
@@ -330,6 +361,9 @@ def test_decode_matches_the_plain_statement(case, wide):
     (24, 8, 8, 128, 64, 0, 3000), (40, 8, 8, 64, 16, 0, 2500), (60, 16, 2, 128, 32, 2000, 4000), (30, 12, 6, 64, 128, 0, 5000),
     (50, 30, 2, 128, 64, 0, 6000), (90, 24, 1, 64, 16, 5000, 9000), (60, 32, 1, 128, 128, 0, 9000), (60, 48, 1, 128, 64, 0, 5000),
     (100, 64, 1, 64, 32, 0, 4000), (256, 12, 12, 128, 64, 0, 129), (1000, 3, 3, 64, 16, 100, 200),
+    (24, 8, 1, 128, 64, 0, 9000), (20, 4, 4, 128, 16, 0, 7000), (64, 12, 12, 128, 64, 1500, 3500), (13, 12, 12, 128, 64, 0, 2040),
+    (12, 12, 12, 64, 64, 0, 1000), (7, 24, 12, 128, 32, 0, 1000), (5, 12, 12, 64, 64, 0, 900), (4, 12, 12, 128, 16, 0, 1500),
+    (1, 12, 12, 64, 16, 0, 2900),
 ])
 def test_decode_many_units_for_each_block(B, H, Hkv, D, P, window, most):
     """Many chunks of keys for each block, so that the ring of stages goes round many times: all requests against 64-bit
