@@ -216,46 +216,63 @@ __global__ void __launch_bounds__(256) kv8_token_kernel(const Kv8TokenParams p) 
 
 // ------------------------------------------------------------------------------------- attention
 //
-// HBM-bound: every visible key's and value's code is read once for all query heads of its key/value
-// head.  At 6.5 TB/s an SM has to take in 23 codes a clock, each of which is converted and multiplied with
+// HBM-bound by its bytes: every visible key's and value's code is read once for all query heads of its
+// key/value head.  At 6.5 TB/s an SM has to take in 23 codes a clock, each of which is converted and multiplied with
 // up to 64 query heads: too much for fp32 lanes, little for the tensor cores, so both products are
 // mma.sync m16n8k16 on fp16 operands (a code is exact in fp16, qhat as well down to 2^-17), fp32 sums.
 // (tcgen05 would need 128-row tiles of one type: the codes converted into shared memory first, or
-// qhat and the weights split into e4m3 parts, for products that are a few percent of the time here.)
+// qhat and the weights split into three e4m3 parts each.  With up to eight heads the products are a few percent
+// of the time; with 32 and more they bound the kernel, see below.)
 //
-// Units.  A unit is a chunk of 128 key positions (aligned) of one request and key/value head.  Units are
-// numbered request by request, head by head, chunk by chunk, and the blocks (one per SM) take equal
+// Units.  A unit is a chunk of 64 key positions (aligned) of one request and key/value head.  Units are
+// numbered request by request, head by head, chunk by chunk, with kKv8ItemCost more at the end of each
+// (request, head) item for what an item costs beside its keys, and the blocks take equal
 // stretches of them, whatever the requests' lengths: every block finds its first unit from the
-// sequence lengths alone, so the host needs no lengths and a captured launch stays valid.  A
-// (request, head) item that one block has whole is finished there; the pieces of one that several
+// sequence lengths alone, so the host needs no lengths and a captured launch stays valid.  An
+// item that one block has whole is finished there; the pieces of one that several
 // blocks share go to the workspace, and the block that arrives last adds them in order (the result
 // does not depend on which one that is).
 //
-// Pipeline.  A producer warp looks up 32 pages at a time and brings each page's codes into a ring of
-// chunk-sized stages by TMA, with the two scales of each 16 keys; eight consumer warps take 16 keys and
-// eight query heads at a time: with G <= 8 heads in a group each warp has one 16-key tile of a chunk,
-// with more the warps are split over the groups of eight heads (NRT of them) and take NRT tiles.
+// Pipeline.  A producer warp looks up a batch of pages at a time (32 boxes, one to a lane) and brings their codes
+// into a ring of chunk-sized stages by TMA, with the scales of each box; items' qhat comes by bulk copy into a
+// ring of its own.  Eight consumer warps take 16 keys and NT groups of eight query heads at a time.  With one
+// set of heads they are two sets of four warps that take chunks in turn, each with its producer (one producer took
+// 0.12 us a chunk and bounded D = 64); with more heads than a warp holds, the warps are shared out over NRG sets of heads.
 //   S^T (16 keys x 8 heads) = K qhat^T: a lane's A operand is 16 (or 32) consecutive bytes of key rows g and
 //   g + 8 (lane = 4 g + t); the features are taken in the order that this gives, qhat's likewise.
 //   O^T (features x 8 heads) += V^T W^T: the bytes of a lane's key pairs are interleaved before the
 //   conversion; W^T is the transpose of S^T's layout, which movmatrix makes.
 // The TMA swizzle (128 bytes; 64 for D = 64) keeps both reads free of bank conflicts (D = 64: two-way).
+// With up to eight heads a warp fits in 96 registers and two blocks in an SM; the loop has none to spare, so the walk
+// through the units lives in shared memory.
 //
 // Softmax.  With x_j = log2(e) qhat . k_j / sqrt(D) and a running reference m, p_j = 2^(x_j - m) is summed in
 // fp32 and w_j = p_j * (value scale) enters the product as fp16 (rounded to 11 bits: off by 2^-12 of each
 // weight, an eighth of the output's own rounding).  m is raised, with one rescaling, only when some
 // x_j + log2(value scale) passes it by more than 2^kSlack: it is at least the first tile's maximum, so
-// weights stay below 2^kSlack and those that fp16 loses are below 2^-24 of the largest.
+// weights stay below 2^kSlack and those that fp16 loses are below 2^-24 of the largest.  With a value scale of
+// 2^e the p_j reach down to 2^-e, so fp32 keeps those above 2^(e - 126) of the largest: 2^-26 at e = 100.
+//
+// Measured (D = 128, lengths from a quarter to all of the most, fractions of 6565 GB/s): 32 requests of up to 16384 tokens, 12
+// heads 192 us, 0.97; of 8192 93 us, 0.88; 48 requests of up to 8192, two key/value heads, one query head each
+// 35 us, eight each 38 us, 0.57.  About 12 us do not depend on the keys: the token kernel and the start behind it 2.4, the
+// units 2, the first table entries and copies 3, joining the warps, arriving and adding the pieces 3.4, the rest the uneven
+// ends.  Bound by the consumers: one key/value head with 16 heads 45, with 32 70, with 64 111 us for the same bytes.
 constexpr int kKv8Chunk = 64;           // key positions of a unit
 constexpr int kKv8Tiles = kKv8Chunk / 16;
 constexpr int kKv8Sms = 148;
 // Blocks of the attention kernel, at most: two per SM where a warp has one group of eight heads, else one.
 __host__ __device__ constexpr int kv8_max_blocks(int G) { return G <= 8 ? 2 * kKv8Sms : kKv8Sms; }
-constexpr int kKv8ItemCost = 4;         // what an item costs beside its units, in units (sharing out the work)
-constexpr int kKv8StepChunks = 48;      // chunks of a block in the one-launch form, at most
-// Units of a block, where there are few.
+// What an item costs beside its units, in units (96 items of up to 8192 tokens, G = 8: 37.4 us, with 2 38.3; 3072 items of 128
+// tokens 34.9, 36.2 with 2, 44.2 with 0).
+constexpr int kKv8ItemCost = 4;
+// Items of at most so many units are not split: adding pieces costs more than the uneven ends (768
+// items of up to 512 tokens: 23.8 us, with 4 26.8).
+constexpr int kKv8Whole = 16;
+// Units of a block, at least, where there are few: the pieces are added by one block, which takes longer with more heads (24
+// items of 1000 tokens, G = 1: 10.9 us by 2, 14.1 by 6; one of 4000, G = 16: 21.5 by 2, 16.6 by 6).
 __host__ __device__ constexpr int kv8_min_share(int G) { return G <= 8 ? 2 : 6; }
-constexpr int kKv8Whole = 16;           // items of at most so many units are not split
+constexpr int kKv8StepChunks = 48;      // chunks of a block in the one-launch form, at most
 constexpr float kSlack = 10.f;          // fp16 holds 2^15
 
 enum : unsigned int { kSiteKv8Full = 83, kSiteKv8Empty = 84 };
@@ -1122,8 +1139,10 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
 // equal share of the item's chunks (pages of at most a chunk: the new token's page, whose scale it may change, is then
 // in the last chunk alone).  While the first codes load, every block forms qhat of its group's heads itself, and the
 // one with the last chunk puts the new token into the cache; the blocks' sums are joined through distributed shared memory.
-// Against the two kernels: no dependent launch and nothing in global memory between the blocks (a d24 request of
-// 301 tokens 9 -> 7 us), but the split follows each item alone, so the GPU is not shared evenly by many ragged ones.
+// Against the two kernels: no dependent launch and nothing in global memory between the blocks (48 items of
+// 1000 tokens, D = 128, 15.0 -> 10.7 us; 288 of 2040 30.7 -> 25.2 us, 15.5 at 6565 GB/s), but the split follows each item alone, so the
+// GPU is not shared evenly by ragged ones.  Latency-bound where items are short (lengths, table, scales and codes follow one
+// another, with the prologue beside them), then by a block's rate of 0.37 us a chunk.
 template <int D>
 __global__ void __launch_bounds__(Kv8StepCfg<D>::THREADS, 2)
     kv8_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Kv8AttnParams p,

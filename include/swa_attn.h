@@ -464,8 +464,8 @@ SWA_API int swa_attn_kv_pages(const int* block_table, const int* kv_len, const i
  * swa_attn_kv8_write: rows kh, vp bf16 (B, T, Hkv, D) (khat and v', as swa_attn_qkv_prologue or the workspace
  * of swa_attn_fwd_ws gives them for positions 0, 1, ...) into the slots of slots, int32 (B, T).  Rows whose
  * slot is negative are skipped; a slot past the cache is recorded (swa_attn_last_device_status) and
- * skipped.  The rows of one call that go into one page must follow one another in row order and in the
- * page (as swa_attn_kv_pages numbers them), and no slot may appear twice: otherwise that page's values are
+ * skipped.  The rows of one call that go into one page must be consecutive rows with consecutive slots
+ * (as swa_attn_kv_pages numbers them; nothing skipped between them): otherwise that page's values are
  * unspecified.  Tokens of a page before the first slot written there must be in the cache already, unless
  * that is the page's token 0.  Nothing but the pages and scales of the slots is written.
  * Errors: SWA_ERR_INVALID_ARG, SWA_ERR_UNSUPPORTED (D not 64 / 128, page_size, n_pages * Hkv * page_size or
@@ -502,7 +502,8 @@ SWA_API int swa_attn_kv8_read(const int* slots, const void* k_cache, const void*
  *   nothing kept between calls; calls that may overlap need one each.
  * A seq_len beyond max_pages * page_size (an empty row) and pages outside the cache (their keys are not
  * visible, a token that belongs there is not stored) are recorded: swa_attn_last_device_status.
- * Scores, exponentials and sums are fp32; the weights enter the products with v_j rounded to 11 bits.
+ * Scores, exponentials and sums are fp32; the weights enter the products with v_j rounded to 11 bits.  Weights
+ * below 2^(e - 126) of the largest are lost where a visible value scale is 2^e (nothing that counts up to e = 100).
  * Errors: SWA_ERR_INVALID_ARG, SWA_ERR_UNSUPPORTED (D not 64 / 128, page_size, H / Hkv > 64, sizes beyond int32),
  * SWA_ERR_MISALIGNED, SWA_ERR_NO_MEMORY (workspace too small), SWA_ERR_CUDA.
  */
