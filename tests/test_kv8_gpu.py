@@ -1,7 +1,10 @@
 """The paged 8-bit cache and the decode step over it on the GPU, against the plain 64-bit statements of
 ``tests/kv8_plain.py`` (tolerances derived there): the allocator and the cached codes have to be equal, outputs are held
 to the rounding of their type and of the weights."""
+import os
 import random
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -661,6 +664,38 @@ def test_steps_in_a_captured_graph():
         assert all(torch.equal(a, b) for a, b in zip(res, eager[i])), i
     assert state[1].tolist() == [20] * 3
     swa.check_device_status()
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing that the first calls set up (launch limits, attributes, the library itself) is in the way of a capture."""
+    code = """
+import torch, causal_sliding_window_swa_b200 as swa
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+B, H, D, P, N = 2, 3, 64, 16, 9
+table, ring = torch.full((B, 4), -1, dtype=torch.int32, device="cuda"), torch.arange(N, dtype=torch.int32, device="cuda")
+kv_len, first, pool, one = i32([0] * B), i32([0] * B), i32([0, N]), i32([1] * B)
+wide = torch.full((B, 4096), -1, dtype=torch.int32, device="cuda")
+q, k, v = (torch.randn((B, H, D), device="cuda").to(torch.bfloat16) for _ in range(3))
+cache = [torch.zeros((N, H, P, D), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in "kv"]
+cache += [torch.ones((N, H), device="cuda") for _ in "kv"]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    slots, n = swa.kv_pages(table, kv_len, first, ring, pool, one, P)
+    out, lse = swa.decode_kv8(q, k, v, *cache, table, n)
+    wide[:, :4].copy_(table)
+    out2, lse2 = swa.decode_kv8(q, None, None, *cache, wide, n)
+    kh, vp = swa.kv8_read(slots, *cache)
+    swa.kv8_write(kh, vp, slots, *cache)
+for _ in range(3):
+    graph.replay()
+swa.check_device_status()
+assert kv_len.tolist() == n.tolist() == [3, 3] and not torch.isnan(out).any()
+assert (out.float() - out2.float()).abs().max() <= (2 ** -7 + 2 ** -10) * out.float().abs().max() and (lse - lse2).abs().max() < 1e-5
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_streams_and_threads():
