@@ -288,6 +288,7 @@ struct Kv8AttnParams {
     int* counters;                // zero at the start
     float* part;                  // [2 * blocks][G][D + 4]: O, then m and l
     int B, H, G, max_pages, W;    // W = 0: no window
+    bool append;                  // the new tokens are written by this step
     float c1;                     // log2(e) / sqrt(D)
     unsigned long long wait_limit_ns;
 };
@@ -698,20 +699,24 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
     };
     auto meta_of = [&](const Boxes& x) { return make_float4(x.ks * p.c1, x.row >= 0 ? x.vs : -1.f, log2f(x.vs), 0.f); };
 
+    // Chunks before the first item's last page: the token kernel leaves them alone, so their codes need not wait for it.
+    const int early = kAppend ? 0 : p.append ? max(0, (((w.n - 1) >> p.c.log_p) << p.c.log_p) / kKv8Chunk - c) : INT_MAX;
     Pages f = look_up();
-    if (!kAppend) {
-        // the new tokens' codes and scales
-        grid_dependency_wait();
-        asm volatile("fence.proxy.async.global;" ::: "memory");
-    }
     Boxes x = find(f);
     f = look_up();
     // the first copies, into an empty ring, do not wait for the scales
     const bool hold = kAppend && append;                       // the last chunk waits for the block's own token
     const int ahead = min(x.chunks - (hold && f.chunks == 0 ? 1 : 0), C::NS);
+    int k0 = part;
+    for (; k0 < min(ahead, early); k0 += C::SETS) copy(x, k0, k0, nullptr);
+    if (!kAppend) {
+        grid_dependency_wait();            // qhat, the new tokens' codes and scales
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        load_scales(x);
+    }
     copy_q(x.item);
     x.item = -1;
-    for (int k = part; k < ahead; k += C::SETS) copy(x, k, k, nullptr);
+    for (; k0 < ahead; k0 += C::SETS) copy(x, k0, k0, nullptr);
     float4 meta = meta_of(x);
     while (next < ahead) {
         const int rel = lane - (next << nb_log);

@@ -1622,7 +1622,7 @@ int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void*
                                 max_pages, counters, swa::kv8_max_blocks(H / Hkv), (double)rope_base, (double)eps};
     const swa::Kv8AttnParams a{reinterpret_cast<const uint2*>(ws + L.qh), block_table, seq_len, doc_start, static_cast<bf*>(out),
                                lse, c, counters, reinterpret_cast<float*>(ws + L.part), B, H, H / Hkv, max_pages,
-                               std::max(0, window), (float)(1.4426950408889634 / std::sqrt((double)D)), wait_limit_ns()};
+                               std::max(0, window), k != nullptr, (float)(1.4426950408889634 / std::sqrt((double)D)), wait_limit_ns()};
     return D == 128 ? launch_kv8_decode<128>(dev, a, t, st) : launch_kv8_decode<64>(dev, a, t, st);
 }
 
