@@ -1,5 +1,5 @@
-"""B200 (sm_100a) causal sliding-window attention (forward, backward, decode): Python binding of the C ABI in
-``include/swa_attn.h``.
+"""B200 (sm_100a) causal sliding-window attention (forward, backward, decode, decode over a paged 8-bit cache):
+Python binding of the C ABI in ``include/swa_attn.h``.
 
 This module only marshals arguments: every step of the layer (RoPE, RMS QK-norm, the value-
 embedding gate, the windowed attention, the log-sum-exp) runs in the CUDA kernels of

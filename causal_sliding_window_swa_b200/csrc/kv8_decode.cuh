@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(256) kv8_token_kernel(const Kv8TokenParams p) 
 //
 // Pipeline.  A producer warp looks up a batch of pages at a time (32 boxes, one to a lane) and brings their codes
 // into a ring of chunk-sized stages by TMA, with the scales of each box; items' qhat comes by bulk copy into a
-// ring of its own.  Eight consumer warps take 16 keys and NT groups of eight query heads at a time.  With one
+// ring of its own.  Copies of pages that take no new token do not wait for the token kernel.  Eight consumer warps take 16 keys and NT groups of eight query heads at a time.  With one
 // set of heads they are two sets of four warps that take chunks in turn, each with its producer (one producer took
 // 0.12 us a chunk and bounded D = 64); with more heads than a warp holds, the warps are shared out over NRG sets of heads.
 //   S^T (16 keys x 8 heads) = K qhat^T: a lane's A operand is 16 (or 32) consecutive bytes of key rows g and
@@ -255,9 +255,9 @@ __global__ void __launch_bounds__(256) kv8_token_kernel(const Kv8TokenParams p) 
 //
 // Measured (D = 128, lengths from a quarter to all of the most, fractions of 6565 GB/s): 32 requests of up to 16384 tokens, 12
 // heads 192 us, 0.97; of 8192 93 us, 0.88; 48 requests of up to 8192, two key/value heads, one query head each
-// 35 us, eight each 38 us, 0.57.  About 12 us do not depend on the keys: the token kernel and the start behind it 2.4, the
+// 35 us, eight each 37 us, 0.58.  About 12 us do not depend on the keys: the token kernel and the start behind it 2.4, the
 // units 2, the first table entries and copies 3, joining the warps, arriving and adding the pieces 3.4, the rest the uneven
-// ends.  Bound by the consumers: one key/value head with 16 heads 45, with 32 70, with 64 111 us for the same bytes.
+// ends.  Bound by the consumers: one key/value head with 16 heads 45, with 32 70, with 64 114 us for the same bytes.
 constexpr int kKv8Chunk = 64;           // key positions of a unit
 constexpr int kKv8Tiles = kKv8Chunk / 16;
 constexpr int kKv8Sms = 148;
