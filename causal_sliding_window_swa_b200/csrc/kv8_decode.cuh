@@ -166,12 +166,13 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 // Place, in groups of four, of features f .. f + 3 (f a multiple of 4) of head h among an item's heads of qhat as the
 // products' B operands, fp16: lane t of a quad takes D/4 consecutive features (kv8_tile), eight of them from each 16 bytes;
-// [head][eights][t].
+// [head][eights][t], a head's eights exchanged in pairs where it is odd: a quad's 64 bytes and the next head's then lie in
+// different banks.
 template <int D>
 __device__ __forceinline__ int kv8_q_place(int h, int f) {
     constexpr int EIGHTS = D / 32;                              // of a lane
     const int eight = f / 8;
-    return ((h * EIGHTS + eight % EIGHTS) * 4 + eight / EIGHTS) * 2 + (f & 4) / 4;
+    return ((h * EIGHTS + (eight % EIGHTS ^ (h & 1))) * 4 + eight / EIGHTS) * 2 + (f & 4) / 4;
 }
 __device__ __forceinline__ uint2 bf16x4_to_half4(uint2 raw) {
     return make_uint2(pack_half2(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u)),
@@ -321,6 +322,7 @@ struct Kv8Cfg {
     static constexpr int SMEM = OFF_BAR + 2 * (NS + MAXQ) * 8 + 1024;     // + alignment slack
     static_assert(NS % SETS == 0, "a stage belongs to one set of warps");
     static_assert(MERGE >= 4096, "the sums of a shared item's pieces");
+    static_assert(OFF_Q % (2 * D) == 0, "a head's operands lie within a multiple of their size");
     static_assert(BLOCKS_PER_SM * (SMEM + 2048) <= 228 * 1024, "shared memory");
 };
 // The attention kernel's and, with room for its own tables, the one-launch form's.
@@ -377,6 +379,11 @@ struct Kv8Shares {
     }
 };
 
+__device__ __forceinline__ uint4 ld_shared_16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
 // Four e4m3 codes -> two pairs of fp16, exact.
 __device__ __forceinline__ void fp8x4_to_half4(uint32_t four, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
@@ -402,11 +409,11 @@ __device__ __forceinline__ float kv8_factor(float m, float l, float M) {
 }
 
 // One tile of 16 keys at position pos0, rows at kr (and `tensor` bytes behind it the values), for NT groups of eight
-// heads.  meta: key scale times c1, value scale, its log2.  q: this lane's qhat operands, of each group's head,
-// 16-byte words four apart.
+// heads.  meta: key scale times c1, value scale, its log2.  q: shared address of this lane's qhat operands, of each group's
+// head: 16-byte words at q ^ 64 i (kv8_q_place).
 template <int D, int NT>
 __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0, int lo, int n, const float4& meta,
-                                         const uint4* const (&q)[NT], float (&o)[NT][D / 16][4], float (&m)[NT][2],
+                                         const uint32_t (&q)[NT], float (&o)[NT][D / 16][4], float (&m)[NT][2],
                                          float (&l)[NT][2], int g, int t) {
     constexpr int NSTEP = D / 16, VW = D / 32;
     const bool whole = pos0 >= lo && pos0 + 16 <= n;
@@ -436,7 +443,7 @@ __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0
     for (int st = 0; st < NSTEP; ++st) {
         if ((st & 1) == 0)
 #pragma unroll
-            for (int x = 0; x < NT; ++x) qs[x] = q[x][st / 2 * 4];
+            for (int x = 0; x < NT; ++x) qs[x] = ld_shared_16(q[x] ^ (st / 2 * 64));
         uint32_t a0, a1, a2, a3;
         fp8x4_to_half4(a[0][st], a0, a2);
         fp8x4_to_half4(a[1][st], a1, a3);
@@ -781,9 +788,12 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
     const int g = lane >> 2, t = lane & 3;
     const int rg = warp % NRG, kslot = warp / NRG;             // set of heads, share of the keys
     const int h_base = rg * C::HEADS;                          // this warp's first head in the group
-    const uint4* q[NT];                                        // heads past the group repeat its last one
+    uint32_t q[NT];                                            // heads past the group repeat its last one
 #pragma unroll
-    for (int x = 0; x < NT; ++x) q[x] = sh.q + ((*turn & ((1 << q_log) - 1)) * p.G + min(h_base + 8 * x + g, p.G - 1)) * (D / 8) + t;
+    for (int x = 0; x < NT; ++x) {
+        const int h = min(h_base + 8 * x + g, p.G - 1);
+        q[x] = smem_u32(sh.q + ((*turn & ((1 << q_log) - 1)) * p.G + h) * (D / 8) + t) ^ (uint32_t)((h & 1) * 64);
+    }
     float o[NT][2 * VW][4];
     float m[NT][2], l[NT][2];                                  // heads 2 t and 2 t + 1 of each group
 #pragma unroll
