@@ -264,8 +264,8 @@ constexpr int kKv8Tiles = kKv8Chunk / 16;
 constexpr int kKv8Sms = 148;
 // Blocks of the attention kernel, at most: two per SM where a warp has one group of eight heads, else one.
 __host__ __device__ constexpr int kv8_max_blocks(int G) { return G <= 8 ? 2 * kKv8Sms : kKv8Sms; }
-// What an item costs beside its units, in units (96 items of up to 8192 tokens, G = 8: 37.4 us, with 2 38.3; 3072 items of 128
-// tokens 34.9, 36.2 with 2, 44.2 with 0).
+// What an item costs beside its units, in units (96 items of up to 8192 tokens, G = 8: 37.4 us, with 2 38.3; 256 requests of 128
+// tokens and 12 heads 34.9, 36.4 with 2, 44.2 with 0).
 constexpr int kKv8ItemCost = 4;
 // Items of at most so many units are not split: adding pieces costs more than the uneven ends (768
 // items of up to 512 tokens: 23.8 us, with 4 26.8).
