@@ -94,8 +94,8 @@ __device__ __forceinline__ uint32_t recode4(uint32_t c, float down) {
 // HBM-bound on prompts, where windows are pages long: the first slot says where the window's next page
 // begins, and the rows from there on are loaded before the other slots are looked at.  W gives each thread
 // four rows of a page (eight of the largest): with fewer, small pages leave too little in flight (16 x 2000 tokens of 12
-// heads, D = 128, pages of 16: 88 us by whole blocks, 48 us so).  16 prompts of 1024 to 2048 tokens, 12 heads, D = 128, pages of 64:
-// 44 us, 34.5 at 6565 GB/s; where they begin inside a page 50 us.  Single tokens are latency-bound: 64 of 12 heads 3.2 us.
+// heads, D = 128, pages of 16: 88 us by whole blocks, 48 us so).  16 prompts of 1024 to 2048 tokens, 12 heads, D = 128, pages
+// of 64: 44 us, 34.5 at 6565 GB/s; where they begin inside a page 50 us.  Single tokens are latency-bound: 64 of 12 heads 3.2 us.
 struct Kv8Store {
     uint8_t* k_cache;
     uint8_t* v_cache;

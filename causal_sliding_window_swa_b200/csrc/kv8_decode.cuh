@@ -236,9 +236,11 @@ __global__ void __launch_bounds__(256) kv8_token_kernel(const Kv8TokenParams p) 
 //
 // Pipeline.  A producer warp looks up a batch of pages at a time (32 boxes, one to a lane) and brings their codes
 // into a ring of chunk-sized stages by TMA, with the scales of each box; items' qhat comes by bulk copy into a
-// ring of its own.  Copies of pages that take no new token do not wait for the token kernel.  Eight consumer warps take 16 keys and NT groups of eight query heads at a time.  With one
-// set of heads they are two sets of four warps that take chunks in turn, each with its producer (one producer took
-// 0.12 us a chunk and bounded D = 64); with more heads than a warp holds, the warps are shared out over NRG sets of heads.
+// ring of its own.  Copies of pages that take no new token do not wait for the token kernel (32 requests of up to
+// 4096 tokens 43.2 -> 41.5 us).  Eight consumer warps take 16 keys and NT groups of eight query heads at a time.
+// With one set of heads they are two sets of four warps that take chunks in turn, each with its producer (one
+// producer took 0.12 us a chunk and bounded D = 64); with more heads than a warp holds, the warps are shared out
+// over NRG sets of heads.
 //   S^T (16 keys x 8 heads) = K qhat^T: a lane's A operand is 16 (or 32) consecutive bytes of key rows g and
 //   g + 8 (lane = 4 g + t); the features are taken in the order that this gives, qhat's likewise.
 //   O^T (features x 8 heads) += V^T W^T: the bytes of a lane's key pairs are interleaved before the
@@ -672,7 +674,9 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
         __syncwarp();
         if (lane == 0) {
             if (meta != nullptr) mbar_arrive_expect_tx(bar, n_load * 2u * box_bytes);
-            else asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n_load * 2u * box_bytes) : "memory");
+            else asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar),
+                              "r"(n_load * 2u * box_bytes)
+                              : "memory");
         }
         __syncwarp();
         if (load) {
@@ -1038,8 +1042,9 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
             at[6] = turn;
         }
         __syncwarp();
-        if (at_ring.ok && !__all_sync(0xffffffffu, mbar_wait(smem_u32(sh.q_full + (turn & ((1 << q_log) - 1))), (uint32_t)(turn >> q_log) & 1u,
-                                                             p.wait_limit_ns, kSiteKv8Full)))
+        const uint32_t q_bar = smem_u32(sh.q_full + (turn & ((1 << q_log) - 1)));
+        if (at_ring.ok &&
+            !__all_sync(0xffffffffu, mbar_wait(q_bar, (uint32_t)(turn >> q_log) & 1u, p.wait_limit_ns, kSiteKv8Full)))
             at_ring.ok = false;
         kv8_piece<D, NT, NRG, C>(p, sh, w, w.ch0 + (u - w.begin), w.ch0 + (end - w.begin), at_ring, at + 6, q_log, warp, lane,
                                  [&](int h, int d4, const float4& O, float M, float L) {
@@ -1155,8 +1160,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
 // in the last chunk alone).  While the first codes load, every block forms qhat of its group's heads itself, and the
 // one with the last chunk puts the new token into the cache; the blocks' sums are joined through distributed shared memory.
 // Against the two kernels: no dependent launch and nothing in global memory between the blocks (48 items of
-// 1000 tokens, D = 128, 15.0 -> 10.7 us; 288 of 2040 30.7 -> 25.2 us, 15.5 at 6565 GB/s), but the split follows each item alone, so the
-// GPU is not shared evenly by ragged ones.  Latency-bound where items are short (lengths, table, scales and codes follow one
+// 1000 tokens, D = 128, 15.0 -> 10.7 us; 288 of 2040 30.7 -> 25.2 us, 15.5 at 6565 GB/s), but the split follows each
+// item alone, so the GPU is not shared evenly by ragged ones.  Latency-bound where items are short (lengths, table, scales and codes follow one
 // another, with the prologue beside them), then by a block's rate of 0.37 us a chunk.
 template <int D>
 __global__ void __launch_bounds__(Kv8StepCfg<D>::THREADS, 2)

@@ -1347,11 +1347,13 @@ int swa_attn_kv_pages(const int* block_table, const int* kv_len, const int* firs
     swa::PagesParams p{block_table, kv_len, first_page, pool, n_new, ring, block_table_out, kv_len_out, first_page_out,
                        pool_out, slots, step_len, B, T, max_pages, n_pages, log_p, std::max(0, window)};
     cudaLaunchConfig_t cfg = {};
-    const bool in_place = block_table == block_table_out || kv_len == kv_len_out || first_page == first_page_out || pool == pool_out;
+    const bool in_place = block_table == block_table_out || kv_len == kv_len_out || first_page == first_page_out ||
+                          pool == pool_out;
     const long long entries = (long long)B * ((long long)max_pages + T);
     // one block for small steps; in place a cluster of eight, else a block for every 2048 entries, eight at least
     // (256512 entries: 4.4 us, 10.7 by eight; 1024 entries: 3.7 by one, 4.0 by eight)
-    const unsigned ranks = entries <= 2048 ? 1u : in_place ? 8u : (unsigned)std::min<long long>(std::max(8ll, entries / 2048), g_num_sms[dev]);
+    const long long shared = std::min<long long>(std::max(8ll, entries / 2048), g_num_sms[dev]);
+    const unsigned ranks = entries <= 2048 ? 1u : in_place ? 8u : (unsigned)shared;
     cfg.gridDim = dim3(ranks);
     cfg.blockDim = dim3(1024);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
@@ -1569,9 +1571,11 @@ int launch_kv8_decode(int dev, const swa::Kv8AttnParams& a, const swa::Kv8TokenP
     // Beyond 16 heads: four groups of eight to a warp where its registers hold their sums (D = 64), else two, the groups shared
     // out over the warps.  32 heads of 128 features: 122 us with four groups (spilled), 70 us with two; 32 of 64: 79 us with four.
     if constexpr (D == 64)
-        return a.G <= 32 ? launch_kv8_attention_n<D, 4, 1>(dev, tk, tv, a, st) : launch_kv8_attention_n<D, 4, 2>(dev, tk, tv, a, st);
+        return a.G <= 32 ? launch_kv8_attention_n<D, 4, 1>(dev, tk, tv, a, st)
+                         : launch_kv8_attention_n<D, 4, 2>(dev, tk, tv, a, st);
     else
-        return a.G <= 32 ? launch_kv8_attention_n<D, 2, 2>(dev, tk, tv, a, st) : launch_kv8_attention_n<D, 2, 4>(dev, tk, tv, a, st);
+        return a.G <= 32 ? launch_kv8_attention_n<D, 2, 2>(dev, tk, tv, a, st)
+                         : launch_kv8_attention_n<D, 2, 4>(dev, tk, tv, a, st);
 }
 
 }  // namespace
@@ -1622,7 +1626,8 @@ int swa_attn_kv8_decode(const void* q, const void* k, const void* v, const void*
                                 max_pages, counters, swa::kv8_max_blocks(H / Hkv), (double)rope_base, (double)eps};
     const swa::Kv8AttnParams a{reinterpret_cast<const uint2*>(ws + L.qh), block_table, seq_len, doc_start, static_cast<bf*>(out),
                                lse, c, counters, reinterpret_cast<float*>(ws + L.part), B, H, H / Hkv, max_pages,
-                               std::max(0, window), k != nullptr, (float)(1.4426950408889634 / std::sqrt((double)D)), wait_limit_ns()};
+                               std::max(0, window), k != nullptr, (float)(1.4426950408889634 / std::sqrt((double)D)),
+                               wait_limit_ns()};
     return D == 128 ? launch_kv8_decode<128>(dev, a, t, st) : launch_kv8_decode<64>(dev, a, t, st);
 }
 
