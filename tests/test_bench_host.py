@@ -97,6 +97,11 @@ def test_recorded_traffic_follows_the_kernel_source(tmp_path, monkeypatch):
     assert bench.recorded_traffic("d24_L_VE") is None                      # the kernel changed since
 
 
+def test_recorded_traffic_is_that_of_the_present_kernel():
+    # the committed capture belongs to the source as it is: where that changes, the figure is taken again
+    assert bench.recorded_traffic("d24_L_VE") > 3e8
+
+
 def _bench(*argv, env=None):
     import os
     import subprocess
