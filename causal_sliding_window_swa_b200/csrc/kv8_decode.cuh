@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(256) kv8_token_kernel(const Kv8TokenParams p) 
 // weight, an eighth of the output's own rounding).  m is raised, with one rescaling, only when some
 // x_j + log2(value scale) passes it by more than 2^kSlack: it is at least the first tile's maximum, so
 // weights stay below 2^kSlack and those that fp16 loses are below 2^-24 of the largest.  With a value scale of
-// 2^e the p_j reach down to 2^-e, so fp32 keeps those above 2^(e - 126) of the largest: 2^-26 at e = 100.
+// 2^e the largest p_j may be 2^-e, so fp32 keeps those above 2^(e - 126) of the largest: 2^-66 at e = 60.
 //
 // Measured (D = 128, lengths from a quarter to all of the most, fractions of 6565 GB/s): 32 requests of up to 16384 tokens, 12
 // heads 192 us, 0.97; of 8192 93 us, 0.88; 48 requests of up to 8192, two key/value heads, one query head each
@@ -405,10 +405,13 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// What a partial sum (m, l) is multiplied with when the reference becomes M: nothing at all where it is empty.
-__device__ __forceinline__ float kv8_factor(float m, float l, float M) {
-    return m == -INFINITY && l == 0.f ? 0.f : ex2_approx(m - M);
+// What a partial sum (m, l) is multiplied with when the reference becomes M, once for each half of the exponent: 0 where the
+// sum is empty.  References contain the value scales, 2^-60 to 2^120, so M - m can pass the 126 binades of one factor while l,
+// up to 2^60 for each key, is still to be kept; O is relative to the largest weight, and what one factor h * h takes from it is nothing.
+__device__ __forceinline__ float kv8_half_factor(float m, float l, float M) {
+    return m == -INFINITY && l == 0.f ? 0.f : ex2_approx(0.5f * (m - M));
 }
+__device__ __forceinline__ float kv8_scale_sum(float l, float half_factor) { return l * half_factor * half_factor; }
 
 // One tile of 16 keys at position pos0, rows at kr (and `tensor` bytes behind it the values), for NT groups of eight
 // heads.  meta: key scale times c1, value scale, its log2.  q: shared address of this lane's qhat operands, of each group's
@@ -472,11 +475,12 @@ __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0
             }
             t0 = fmaxf(t0, m[x][0]);
             t1 = fmaxf(t1, m[x][1]);
-            const float f0 = ex2_approx(m[x][0] - t0), f1 = ex2_approx(m[x][1] - t1);
+            const float h0 = ex2_approx(0.5f * (m[x][0] - t0)), h1 = ex2_approx(0.5f * (m[x][1] - t1));
+            const float f0 = h0 * h0, f1 = h1 * h1;
             m[x][0] = t0;
             m[x][1] = t1;
-            l[x][0] *= f0;
-            l[x][1] *= f1;
+            l[x][0] = kv8_scale_sum(l[x][0], h0);
+            l[x][1] = kv8_scale_sum(l[x][1], h1);
 #pragma unroll
             for (int k = 0; k < 2 * VW; ++k) {
                 o[x][k][0] *= f0;
@@ -880,7 +884,8 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
                     const int at = place + 4 * x + t;
                     const float m2 = sh.m[at], l2 = sh.l[at];
                     const float M = fmaxf(m[x][e], m2);
-                    const float f1 = kv8_factor(m[x][e], l[x][e], M), f2 = kv8_factor(m2, l2, M);
+                    const float h1 = kv8_half_factor(m[x][e], l[x][e], M), h2 = kv8_half_factor(m2, l2, M);
+                    const float f1 = h1 * h1, f2 = h2 * h2;
 #pragma unroll
                     for (int k = 0; k < 2 * VW; ++k) {
                         const float2 o2 = *reinterpret_cast<const float2*>(sh.o + at * PITCH + 16 * k + 2 * g);
@@ -888,7 +893,7 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
                         o[x][k][2 + e] = o[x][k][2 + e] * f1 + o2.y * f2;
                     }
                     m[x][e] = M;
-                    l[x][e] = l[x][e] * f1 + l2 * f2;
+                    l[x][e] = kv8_scale_sum(l[x][e], h1) + kv8_scale_sum(l2, h2);
                 }
                 __syncwarp();
                 put();                     // where it has just read
@@ -911,10 +916,10 @@ __device__ __forceinline__ void kv8_piece(const Kv8AttnParams& p, const Kv8Share
                 const float* src = sh.o + y * PITCH + 16 * (2 * (d4 % VW)) + 2 * (d4 / VW);
 #pragma unroll
                 for (int k = 0; k < SLOTS; ++k) {
-                    const float lk = sh.l[y + k * STEP], f = kv8_factor(mk[k], lk, M);
+                    const float lk = sh.l[y + k * STEP], h = kv8_half_factor(mk[k], lk, M), f = h * h;
                     const float2 a = *reinterpret_cast<const float2*>(src + k * STEP * PITCH);
                     const float2 b = *reinterpret_cast<const float2*>(src + k * STEP * PITCH + 16);
-                    L = fmaf(lk, f, L);
+                    L += kv8_scale_sum(lk, h);
                     O.x = fmaf(a.x, f, O.x);
                     O.y = fmaf(a.y, f, O.y);
                     O.z = fmaf(b.x, f, O.z);
@@ -1101,8 +1106,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
                             }
                         }
                         const float M2 = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
-                        const float f0 = kv8_factor(M, L, M2);
-                        L *= f0;
+                        const float h0 = kv8_half_factor(M, L, M2), f0 = h0 * h0;
+                        L = kv8_scale_sum(L, h0);
                         O.x *= f0;
                         O.y *= f0;
                         O.z *= f0;
@@ -1110,8 +1115,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
                         M = M2;
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
-                            const float f = kv8_factor(ml[y].x, ml[y].y, M);
-                            L = fmaf(ml[y].y, f, L);
+                            const float h = kv8_half_factor(ml[y].x, ml[y].y, M), f = h * h;
+                            L += kv8_scale_sum(ml[y].y, h);
                             O.x = fmaf(v[y].x, f, O.x);
                             O.y = fmaf(v[y].y, f, O.y);
                             O.z = fmaf(v[y].z, f, O.z);
@@ -1136,9 +1141,9 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
                         for (int k = 0; k < share; ++k) M = fmaxf(M, sh.m[k * p.G + h]);
                         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
                         for (int k = 0; k < share; ++k) {
-                            const float f = kv8_factor(sh.m[k * p.G + h], sh.l[k * p.G + h], M);
+                            const float lk = sh.l[k * p.G + h], hf = kv8_half_factor(sh.m[k * p.G + h], lk, M), f = hf * hf;
                             const float4 v = s_sum[k * n_out + threadIdx.x];
-                            L = fmaf(sh.l[k * p.G + h], f, L);
+                            L += kv8_scale_sum(lk, hf);
                             O.x = fmaf(v.x, f, O.x);
                             O.y = fmaf(v.y, f, O.y);
                             O.z = fmaf(v.z, f, O.z);
@@ -1255,8 +1260,8 @@ __global__ void __launch_bounds__(Kv8StepCfg<D>::THREADS, 2)
 #pragma unroll
         for (int k = 0; k < kDecodeMaxCluster; ++k) {
             if (k >= ranks) break;
-            const float f = kv8_factor(mk[k], lk[k], M);
-            L = fmaf(lk[k], f, L);
+            const float hf = kv8_half_factor(mk[k], lk[k], M), f = hf * hf;
+            L += kv8_scale_sum(lk[k], hf);
             O.x = fmaf(ld_shared_cluster_f32(pt + 4 * d4, k), f, O.x);
             O.y = fmaf(ld_shared_cluster_f32(pt + 4 * d4 + 1, k), f, O.y);
             O.z = fmaf(ld_shared_cluster_f32(pt + 4 * d4 + 2, k), f, O.z);
