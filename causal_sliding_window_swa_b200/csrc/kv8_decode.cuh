@@ -250,10 +250,15 @@ __global__ void __launch_bounds__(256) kv8_token_kernel(const Kv8TokenParams p) 
 // through the units lives in shared memory.
 //
 // Softmax.  With x_j = log2(e) qhat . k_j / sqrt(D) and a running reference m, p_j = 2^(x_j - m) is summed in
-// fp32 and w_j = p_j * (value scale) enters the product as fp16 (rounded to 11 bits: off by 2^-12 of each
+// fp32 and w_j = p_j * (value scale) enters the product as fp16 (rounded to 11 bits: off by at most 2^-11 of each
 // weight, an eighth of the output's own rounding).  m is raised, with one rescaling, only when some
-// x_j + log2(value scale) passes it by more than 2^kSlack: it is at least the first tile's maximum, so
-// weights stay below 2^kSlack and those that fp16 loses are below 2^-24 of the largest.  With a value scale of
+// x_j + log2(value scale) passes it by more than kSlack: it is at least the first tile's maximum, so the largest
+// 2^5 w_j, which is what the product takes, lies between 2^5 and 2^15.  A key that weighs little may still be all that counts (one
+// that outweighs it may have values of zero, or values in other features), so weights that fp16 would hold in fewer bits are
+// multiplied apart, times 2^15, with the codes times 2^-15 (exact in fp16): 11 bits down to 2^-34 of the largest weight, and
+// half a step of 2^-45 of it below.  Scores of rows with unit root mean square lie within 33 binades.  A tile with such a weight
+// has twice the products with v: where all have, 32 requests of up to 16384 tokens 178 us against 173, 48 of one key/value head
+// with 16 heads 48.4 against 44.7.  The test for it takes about 1% (2 to 3% with few keys or 32 heads).  With a value scale of
 // 2^e the largest p_j may be 2^-e, so fp32 keeps those above 2^(e - 126) of the largest: 2^-66 at e = 60.
 //
 // Measured (D = 128, lengths from a quarter to all of the most, fractions of 6565 GB/s): 32 requests of up to 16384 tokens, 12
@@ -276,7 +281,9 @@ constexpr int kKv8Whole = 16;
 // items of 1000 tokens, G = 1: 10.9 us by 2, 14.1 by 6; one of 4000, G = 16: 21.5 by 2, 16.6 by 6).
 __host__ __device__ constexpr int kv8_min_share(int G) { return G <= 8 ? 2 : 6; }
 constexpr int kKv8StepChunks = 48;      // chunks of a block in the one-launch form, at most
-constexpr float kSlack = 10.f;          // fp16 holds 2^15
+constexpr float kSlack = 10.f;
+constexpr float kWeightUp = 32.f;       // weights enter the products times 2^5: up to 2^15, which fp16 holds
+constexpr float kHalfLeast = 0x1p-14f;  // fp16 has 11 bits from here on
 
 enum : unsigned int { kSiteKv8Full = 83, kSiteKv8Empty = 84 };
 
@@ -393,6 +400,11 @@ __device__ __forceinline__ void fp8x4_to_half4(uint32_t four, uint32_t& lo, uint
         : "=r"(lo), "=r"(hi)
         : "r"(four));
 }
+// Two fp16 times 2^-15: exact for codes, whose smallest step is 2^-9.
+__device__ __forceinline__ uint32_t half2_down15(uint32_t x) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(0x1p-15f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 // 8x8 matrix of 16-bit elements held two to a lane (row lane / 4), transposed.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t r;
@@ -416,6 +428,7 @@ __device__ __forceinline__ float kv8_scale_sum(float l, float half_factor) { ret
 // One tile of 16 keys at position pos0, rows at kr (and `tensor` bytes behind it the values), for NT groups of eight
 // heads.  meta: key scale times c1, value scale, its log2.  q: shared address of this lane's qhat operands, of each group's
 // head: 16-byte words at q ^ 64 i (kv8_q_place).
+// meta.y is the value scale times kWeightUp.
 template <int D, int NT>
 __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0, int lo, int n, const float4& meta,
                                          const uint32_t (&q)[NT], float (&o)[NT][D / 16][4], float (&m)[NT][2],
@@ -456,10 +469,11 @@ __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0
         for (int x = 0; x < NT; ++x)
             mma_16816(sc[x][st % NC], a0, a1, a2, a3, (st & 1) ? qs[x].z : qs[x].x, (st & 1) ? qs[x].w : qs[x].y);
     }
-    uint32_t b[NT][2];
+    float w[NT][4];                                        // the weights: keys g and g + 8, heads 2 t and 2 t + 1
+    float least = INFINITY;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-        float s[4];                                        // keys g and g + 8, heads 2 t and 2 t + 1
+        float s[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[e] = (NC == 2 ? sc[x][0][e] + sc[x][NC - 1][e] : sc[x][0][e]) * meta.x;
         if (!whole) {
@@ -493,8 +507,11 @@ __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0
         for (int e = 0; e < 4; ++e) s[e] = ex2_approx(s[e] - m[x][e & 1]);
         l[x][0] += s[0] + s[2];
         l[x][1] += s[1] + s[3];
-        b[x][0] = movmatrix_trans(pack_half2(s[0] * meta.y, s[1] * meta.y));
-        b[x][1] = movmatrix_trans(pack_half2(s[2] * meta.y, s[3] * meta.y));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[x][e] = s[e] * meta.y;
+            least = fminf(least, w[x][e]);
+        }
     }
     uint32_t v[4][VW];                                     // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
 #pragma unroll
@@ -522,20 +539,62 @@ __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0
                 for (int k = 0; k < VW; ++k) v[x][k] = 0u;
         }
     }
-#pragma unroll
-    for (int k = 0; k < VW; ++k) {
-        // features 4 k .. 4 k + 3 of this lane, keys (2 t, 2 t + 1) and (2 t + 8, 2 t + 9)
-        uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
-        fp8x4_to_half4(__byte_perm(v[0][k], v[1][k], 0x5140), a0, a1);
-        fp8x4_to_half4(__byte_perm(v[2][k], v[3][k], 0x5140), a2, a3);
-        fp8x4_to_half4(__byte_perm(v[0][k], v[1][k], 0x7362), c0, c1);
-        fp8x4_to_half4(__byte_perm(v[2][k], v[3][k], 0x7362), c2, c3);
+    // O^T, with the small weights apart where there are any
+    auto add = [&](auto split) {
+        constexpr bool kSplit = decltype(split)::value;
+        uint32_t b[NT][2], b_small[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-            mma_16816(o[x][2 * k], a0, a1, a2, a3, b[x][0], b[x][1]);
-            mma_16816(o[x][2 * k + 1], c0, c1, c2, c3, b[x][0], b[x][1]);
+            float up[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                up[e] = w[x][e] < kHalfLeast ? w[x][e] * 0x1p15f : 0.f;
+                if (kSplit && w[x][e] < kHalfLeast) w[x][e] = 0.f;
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                b[x][r] = movmatrix_trans(pack_half2(w[x][2 * r], w[x][2 * r + 1]));
+                if (kSplit) b_small[x][r] = movmatrix_trans(pack_half2(up[2 * r], up[2 * r + 1]));
+            }
         }
+#pragma unroll
+        for (int k = 0; k < VW; ++k) {
+            // features 4 k .. 4 k + 3 of this lane, keys (2 t, 2 t + 1) and (2 t + 8, 2 t + 9)
+            uint32_t a[2][4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int bytes = y == 0 ? 0x5140 : 0x7362;
+                fp8x4_to_half4(__byte_perm(v[0][k], v[1][k], bytes), a[y][0], a[y][1]);
+                fp8x4_to_half4(__byte_perm(v[2][k], v[3][k], bytes), a[y][2], a[y][3]);
+            }
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) mma_16816(o[x][2 * k + y], a[y][0], a[y][1], a[y][2], a[y][3], b[x][0], b[x][1]);
+            if (kSplit) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[y][e] = half2_down15(a[y][e]);
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        mma_16816(o[x][2 * k + y], a[y][0], a[y][1], a[y][2], a[y][3], b_small[x][0], b_small[x][1]);
+            }
+        }
+    };
+    bool split = __any_sync(0xffffffffu, least < kHalfLeast);
+    if (split && !whole) {                                 // not for the keys that are not visible, whose weights are 0
+        bool small = false;
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) small = small || (w[x][e] > 0.f && w[x][e] < kHalfLeast);
+        split = __any_sync(0xffffffffu, small);
     }
+    if (split) add(std::true_type{});
+    else add(std::false_type{});
 }
 
 // Four features of the result, and its log-sum-exp: O / L, or an empty row where no key was visible (all on pages
@@ -544,7 +603,7 @@ template <int D>
 __device__ __forceinline__ void kv8_store4(const Kv8AttnParams& p, int b, int hk, int h, int d4, const float4& O, float M,
                                            float L) {
     const long long row = (long long)b * p.H + (long long)hk * p.G + h;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float inv = L == 0.f ? 0.f : (1.f / kWeightUp) / L;
     *reinterpret_cast<uint2*>(p.out + row * D + 4 * d4) =
         make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
     if (d4 == 0 && p.lse != nullptr) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
@@ -712,7 +771,7 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
         }
         return true;
     };
-    auto meta_of = [&](const Boxes& x) { return make_float4(x.ks * p.c1, x.row >= 0 ? x.vs : -1.f, log2f(x.vs), 0.f); };
+    auto meta_of = [&](const Boxes& x) { return make_float4(x.ks * p.c1, x.row >= 0 ? kWeightUp * x.vs : -1.f, log2f(x.vs), 0.f); };
 
     // Chunks before the first item's last page: the token kernel leaves them alone, so their codes need not wait for it.
     const int early = kAppend ? 0 : p.append ? max(0, (((w.n - 1) >> p.c.log_p) << p.c.log_p) / kKv8Chunk - c) : INT_MAX;

@@ -502,7 +502,8 @@ SWA_API int swa_attn_kv8_read(const int* slots, const void* k_cache, const void*
  *   nothing kept between calls; calls that may overlap need one each.
  * A seq_len beyond max_pages * page_size (an empty row) and pages outside the cache (their keys are not
  * visible, a token that belongs there is not stored) are recorded: swa_attn_last_device_status.
- * Scores, exponentials and sums are fp32; the weights enter the products with v_j rounded to 11 bits.  Weights
+ * Scores, exponentials p_j and sums are fp32.  The products with v_j take p_j * (value scale) in 11 bits (off by at
+ * most 2^-11 of it); below 2^-34 of the largest of these of a request and head, off by at most 2^-45 of that one.  p_j
  * below 2^(e - 126) of the largest are lost where the largest visible value scale is 2^e: 2^-66 of it at e = 60.
  * Errors: SWA_ERR_INVALID_ARG, SWA_ERR_UNSUPPORTED (D not 64 / 128, page_size, H / Hkv > 64, sizes beyond int32),
  * SWA_ERR_MISALIGNED, SWA_ERR_NO_MEMORY (workspace too small), SWA_ERR_CUDA.

@@ -1,4 +1,5 @@
-"""The decode step over the paged 8-bit cache where value scales span many powers of two: pages of zeros beside pages of
+"""The decode step over the paged 8-bit cache where weights and value scales span many powers of two: keys that weigh little
+beside one that contributes nothing, pages whose large values lie in features of their own, pages of zeros beside pages of
 very large values.  In 64 bits against the cached values, as kv8_read returns them; tolerances as in ``tests/kv8_plain.py``,
 which counts an error of 2^-11 for each weight, whatever its size."""
 import numpy as np
@@ -65,6 +66,38 @@ def check(*a, **kw):
 # One launch (a narrow table, few keys) or two; one group of eight heads, several in a warp, several sets of warps.
 FORMS = [(128, 1, 0, 700), (128, 1, 8192, 700), (128, 1, 0, 16384), (64, 2, 0, 1500), (64, 8, 8192, 16384), (128, 12, 0, 3000),
          (128, 32, 0, 3000), (128, 64, 0, 2000), (64, 32, 0, 3000), (64, 64, 0, 2000)]
+
+
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("bits", [12.0, 20.4, 25.5, 31.0])
+@pytest.mark.parametrize("D,G,wide,n", FORMS)
+def test_a_key_without_values_outweighs_the_others(D, G, wide, n, bits, where):
+    # one key with values of zero scores `bits` powers of two above all others (rows of unit root mean square
+    # score 16 above and below zero at most, 12 with 64 features): the others are all that the output consists of.  Their values are
+    # positive, so that errors of their weights, all alike, do not cancel
+    g = torch.Generator().manual_seed(n + G)
+    top = D ** 0.5 * 1.4426950408889634                    # score of the query's direction itself, in powers of two
+    alpha = torch.full((n,), 1 - bits / top)
+    v = torch.rand((n, D), generator=g) + 0.5
+    at = {"first": 0, "middle": n // 2 + 5, "last": n - 1}[where]
+    alpha[at], v[at] = 1.0, 0.0
+    ref = check(alpha, v, D, G, wide)
+    assert (ref > 0).all()
+
+
+@pytest.mark.parametrize("exponent", [10, 24, 33])
+@pytest.mark.parametrize("page", [0, 7, -1])
+@pytest.mark.parametrize("D,G,wide,n", FORMS)
+def test_pages_whose_values_lie_in_other_features(D, G, wide, n, page, exponent):
+    # equal scores; one page has a value of 2^exponent in one feature and zeros elsewhere, all others have nothing there
+    g = torch.Generator().manual_seed(n + G + 1)
+    v = torch.rand((n, D), generator=g) + 0.5
+    v[:, 5] = 0.0
+    at = page % (n // P) * P
+    v[at:at + P] = 0.0
+    v[at + 3, 5] = 2.0 ** exponent
+    ref = check(torch.full((n,), 0.1), v, D, G, wide)
+    assert (ref[:, [f for f in range(D) if f != 5]] > 0.4).all()
 
 
 @pytest.mark.parametrize("kind", ["zeros first", "zeros last", "zeros in every second chunk", "zeros in every second page",
