@@ -341,8 +341,9 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const int* __restrict__ s
 //   else:  pages [F, f) go back, f = max(F, floor(max(0, L - W + 1) / P)): the next query is at
 //          position L or later and sees no key before L - W + 1.  (W = 0: none.)
 //          need = ceil((L + n) / P) - have, 0 where the request cannot be served at all (n > T, more
-//          than max_pages pages, L < 0); S = inclusive sum of need in request order; the request is served
+//          than max_pages pages); S = inclusive sum of need in request order; the request is served
 //          iff n > 0 and (need = 0 or S <= free).
+//   L < 0, L > max_pages * P, F < 0 or F > have: nothing of the request changes, whatever n is.
 // A request that finds no page therefore holds back later ones that need one (their order is kept),
 // and since S only grows the served requests' pages are the first taken ones of the ring.
 // The free pages are ring[(head + i) mod n_pages], i < free; pages given back are appended behind

@@ -442,8 +442,10 @@ SWA_API int swa_attn_bwd(const void* q, const void* k, const void* v, const void
  *   need_b = ceil((L + n) / P) - ceil(L / P) pages are taken.  Request b is served iff n >= 1 and either
  *     need_b = 0 or the sum of need over requests 0 .. b is at most `free`: requests are served in order, one that
  *     finds no page holds back those after it that need one, and pages given back in a step are free from the
- *     next step on.  A request that cannot be served at all (n > T, more than max_pages pages, or a
- *     kv_len or first_page that is not possible) is left as it was and holds nobody back.
+ *     next step on.  A request that cannot be served at all (n > T, more than max_pages pages) takes nothing and
+ *     holds nobody back; like an idle one it gives back the pages that its window has passed.  One whose kv_len or
+ *     first_page is not possible (kv_len outside 0 .. max_pages * page_size, first_page outside 0 .. its number of
+ *     pages) is left as it was.
  * Results (each may be the array it follows from, for a step in place; other overlaps are not allowed):
  *   block_table_out, kv_len_out, first_page_out, pool_out   the state after the step (ring is always updated in
  *               place: only entries outside the free stretch change, so a step can be repeated from

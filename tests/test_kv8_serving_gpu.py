@@ -1,5 +1,6 @@
 """The paged 8-bit cache as a server uses it: decode steps of the two-launch form, whose long requests are shared out among
-blocks, captured and replayed with new tokens, from several threads and in graphs that run at the same time."""
+blocks, captured and replayed with new tokens, from several threads and in graphs that run at the same time; allocator steps
+that cannot serve a request."""
 import threading
 
 import pytest
@@ -145,4 +146,38 @@ def test_two_launch_steps_from_threads_and_streams(H, Hkv, D, P):
     [t.start() for t in ts]
     [t.join() for t in ts]
     assert all(len(r) == 10 and torch.equal(o, out) and torch.equal(l, lse) for r in got for o, l in r)
+    swa.check_device_status()
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("T", [1, 40, 2000])
+def test_requests_that_cannot_be_served_still_give_back_what_their_window_has_passed(T, in_place):
+    """Window 20, pages of 16, 5 table entries.  Requests: more new tokens than T; more pages than the table has; idle; served; a
+    first_page that is not possible; a kv_len that is not possible; an impossible one that has ended."""
+    L, F = [64, 80, 64, 64, 50, 81, -1], [1, 0, 0, 0, 5, 0, 0]
+    news = [T + 1, 1, 0, 1, 1, 1, -1]
+    table = torch.full((7, 5), -1, dtype=torch.int32)
+    page = iter(range(100))
+    for b in range(7):
+        for j in range(max(0, F[b]), min(5, -(-max(0, L[b]) // 16))):
+            table[b, j] = next(page)
+    held = next(page)
+    N = held + 6
+    ring = torch.arange(N, dtype=torch.int32).roll(-held).cuda()          # free: pages held .. N - 1
+    state = [table.cuda(), i32(L), i32(F), i32([0, 6])]
+    out = None if in_place else tuple(torch.full_like(t, -7) for t in state)
+    slots, step_len = swa.kv_pages(state[0], state[1], state[2], ring, state[3], i32(news), 16, 20, T, out=out)
+    got = [t.tolist() for t in (out or state)]
+    # pages before max(0, L - 19) // 16 go back: entries 1 of the first, 0 .. 2 of the second, 0 and 1 of the next two
+    want = table.clone()
+    back = []
+    for b, upto in ((0, 2), (1, 3), (2, 2), (3, 2)):
+        back += want[b, F[b]:upto].tolist()
+        want[b, F[b]:upto] = -1
+    want[3, 4] = held
+    assert got[0] == want.tolist() and got[1] == [64, 80, 64, 65, 50, 81, -1] and got[2] == [2, 3, 2, 2, 5, 0, 0]
+    assert got[3] == [1, 6 - 1 + len(back)] and len(back) == 8
+    assert ring.tolist()[6:14] == back and ring.tolist()[:6] == list(range(held, N))
+    assert step_len.tolist() == [0, 0, 0, 65, 0, 0, 0] and slots[3, 0] == held * 16
+    assert (slots.cpu().flatten() >= 0).sum() == 1
     swa.check_device_status()
