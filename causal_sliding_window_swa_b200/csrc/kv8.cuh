@@ -11,7 +11,7 @@
 // lets the scale of a page that is still being filled grow without loss: dividing a code by a power
 // of two is exact unless it falls below 2^-6, where it is off by at most half of 2^-9.  So a page
 // filled token by token holds what one write of all its tokens leaves, except for elements that fall there, which
-// may be rounded twice: amax is above 224 * 2^e, so they are smaller than amax * 2^-6 / 224, or 2^-13.8 of it.
+// may be rounded more than once: amax is above 224 * 2^e, so they are smaller than amax * 2^-6 / 224, or 2^-13.8 of it.
 //
 // Operations here: kv_pages_* (which pages a request's tokens live in), kv8_write_kernel (bf16 khat
 // and v' rows into the pages), kv8_read_kernel (the reverse).

@@ -771,7 +771,10 @@ __device__ __forceinline__ void kv8_produce(const CUtensorMap& tm_k, const CUten
         }
         return true;
     };
-    auto meta_of = [&](const Boxes& x) { return make_float4(x.ks * p.c1, x.row >= 0 ? kWeightUp * x.vs : -1.f, log2f(x.vs), 0.f); };
+    // (a scale of zero, which no write leaves, counts as the smallest in the reference: its keys have values of zero)
+    auto meta_of = [&](const Boxes& x) {
+        return make_float4(x.ks * p.c1, x.row >= 0 ? kWeightUp * x.vs : -1.f, fmaxf(log2f(x.vs), (float)kEMin), 0.f);
+    };
 
     // Chunks before the first item's last page: the token kernel leaves them alone, so their codes need not wait for it.
     const int early = kAppend ? 0 : p.append ? max(0, (((w.n - 1) >> p.c.log_p) << p.c.log_p) / kKv8Chunk - c) : INT_MAX;

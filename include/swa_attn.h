@@ -420,7 +420,8 @@ SWA_API int swa_attn_bwd(const void* q, const void* k, const void* v, const void
  * Caller-owned, 16-byte (scales: 4-byte) aligned; n_pages * Hkv * P < 2^31.  Slot s of a cache is token
  * s % P of page s / P.  Nothing has to be initialised: a page's scale starts anew with its token 0.
  * While a page fills, its scale grows where a new token needs it, and the codes already there are moved
- * to the new scale: exactly, but for values below 2^-13 of the page's largest, which are rounded again.
+ * to the new scale: exactly, but for values below 2^-13 of the page's largest, which are rounded again (each time by
+ * half of 2^-9 of the scale at most: in all less than 2^-8 of the last one).
  * Caching rounds a value to 4 significant bits (half a step is 2^-4 of it, or 2^-10 of the scale).
  * An infinity becomes the largest code at the largest scale, 2^120; a NaN stays a NaN and does not
  * count towards the scale.

@@ -28,7 +28,7 @@ def bf16(x):
     return torch.from_numpy(np.ldexp(np.rint(m * 256), e - 8)).to(torch.bfloat16)
 
 
-def run(alpha, v, D, G, wide, seed=0):
+def run(alpha, v, D, G, wide, seed=0, change=None):
     """One request of n keys, one key/value head: key j is alpha[j] times the query's direction, its values v[j] (n, D).
     The step's out (G, D) and lse (G), and those in 64 bits with the tolerances of each."""
     n = len(alpha)
@@ -46,6 +46,8 @@ def run(alpha, v, D, G, wide, seed=0):
     cache += [torch.full((n_pages, 1), float("nan"), device="cuda") for _ in "kv"]
     swa.kv8_write(kh.to(torch.bfloat16)[None, :, None].contiguous().cuda(), v.to(torch.bfloat16)[None, :, None].contiguous().cuda(),
                   slots, *cache)
+    if change is not None:
+        change(order, *cache)
     table = torch.full((1, n_pages + wide), -1, dtype=torch.int32)
     table[0, :n_pages] = order.int()
     out, lse = swa.decode_kv8(q, None, None, *cache, table.cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"))
@@ -114,3 +116,18 @@ def test_pages_of_zeros_beside_pages_of_large_values(D, G, wide, n, exponent, ki
     v = (torch.rand((n, D), generator=g) + 0.5) * 2.0 ** exponent
     v[zero] = 0.0
     check(torch.full((n,), 0.1), v, D, G, wide)
+
+
+@pytest.mark.parametrize("D,G,wide,n", FORMS)
+def test_pages_whose_scale_is_zero_have_values_of_zero(D, G, wide, n):
+    # no write leaves such a scale, but a cache that starts as zeros has it, and value = code * scale as in kv8_read
+    g = torch.Generator().manual_seed(n + G + 3)
+
+    def change(order, k_cache, v_cache, k_scale, v_scale):
+        v_scale[order[::2]] = 0.0
+        k_scale[order[::3]] = 0.0
+
+    ref = check(torch.full((n,), 0.1), torch.rand((n, D), generator=g) + 0.5, D, G, wide, change=change)
+    assert (ref > 0.4).all()
+    ref = check(torch.full((n,), 0.1), torch.rand((n, D), generator=g), D, G, wide, change=lambda order, *c: c[3].zero_())
+    assert (ref == 0).all()
