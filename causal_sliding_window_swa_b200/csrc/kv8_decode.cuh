@@ -262,10 +262,10 @@ __global__ void __launch_bounds__(256) kv8_token_kernel(const Kv8TokenParams p) 
 // 2^e the largest p_j may be 2^-e, so fp32 keeps those above 2^(e - 126) of the largest: 2^-66 at e = 60.
 //
 // Measured (D = 128, lengths from a quarter to all of the most, fractions of 6565 GB/s): 32 requests of up to 16384 tokens, 12
-// heads 192 us, 0.97; of 8192 93 us, 0.88; 48 requests of up to 8192, two key/value heads, one query head each
+// heads 194 us, 0.95; of 8192 93 us, 0.88; 48 requests of up to 8192, two key/value heads, one query head each
 // 35 us, eight each 37 us, 0.58.  About 12 us do not depend on the keys: the token kernel and the start behind it 2.4, the
 // units 2, the first table entries and copies 3, joining the warps, arriving and adding the pieces 3.4, the rest the uneven
-// ends.  Bound by the consumers: one key/value head with 16 heads 45, with 32 70, with 64 114 us for the same bytes.
+// ends.  Bound by the consumers: one key/value head with 16 heads 45, with 32 72, with 64 114 us for the same bytes.
 constexpr int kKv8Chunk = 64;           // key positions of a unit
 constexpr int kKv8Tiles = kKv8Chunk / 16;
 constexpr int kKv8Sms = 148;
@@ -419,7 +419,8 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 }
 // What a partial sum (m, l) is multiplied with when the reference becomes M, once for each half of the exponent: 0 where the
 // sum is empty.  References contain the value scales, 2^-60 to 2^120, so M - m can pass the 126 binades of one factor while l,
-// up to 2^60 for each key, is still to be kept; O is relative to the largest weight, and what one factor h * h takes from it is nothing.
+// up to 2^60 for each key, is still to be kept; O is relative to the largest weight, and what one factor h * h takes from it
+// is nothing.
 __device__ __forceinline__ float kv8_half_factor(float m, float l, float M) {
     return m == -INFINITY && l == 0.f ? 0.f : ex2_approx(0.5f * (m - M));
 }
@@ -1228,8 +1229,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<D, NT, NRG>::THREADS, Kv8AttnCfg<D,
 // one with the last chunk puts the new token into the cache; the blocks' sums are joined through distributed shared memory.
 // Against the two kernels: no dependent launch and nothing in global memory between the blocks (48 items of
 // 1000 tokens, D = 128, 15.0 -> 10.7 us; 288 of 2040 30.7 -> 25.2 us, 15.5 at 6565 GB/s), but the split follows each
-// item alone, so the GPU is not shared evenly by ragged ones.  Latency-bound where items are short (lengths, table, scales and codes follow one
-// another, with the prologue beside them), then by a block's rate of 0.37 us a chunk.
+// item alone, so the GPU is not shared evenly by ragged ones.  Latency-bound where items are short (lengths, table, scales and
+// codes follow one another, with the prologue beside them), then by a block's rate of 0.37 us a chunk.
 template <int D>
 __global__ void __launch_bounds__(Kv8StepCfg<D>::THREADS, 2)
     kv8_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Kv8AttnParams p,
