@@ -326,7 +326,7 @@ struct Kv8Cfg {
     static constexpr int OFF_Q = OFF_ML + 2 * CONSUMERS * HEADS * 4;      // items' qhat operands: two of the largest, or more
     static constexpr int QBYTES = 2 * NTG * 8 * D * 2;
     static constexpr int MAXQ = 8;                               // items in that ring, at most
-    static constexpr int OFF_META = OFF_Q + QBYTES;              // per stage and tile: ks c1, vs, log2 vs, pad
+    static constexpr int OFF_META = OFF_Q + QBYTES;              // per stage and tile: ks c1, 2^5 vs, log2 vs, pad
     static constexpr int OFF_BAR = OFF_META + NS * kKv8Tiles * 16;
     static constexpr int SMEM = OFF_BAR + 2 * (NS + MAXQ) * 8 + 1024;     // + alignment slack
     static_assert(NS % SETS == 0, "a stage belongs to one set of warps");
@@ -427,9 +427,8 @@ __device__ __forceinline__ float kv8_half_factor(float m, float l, float M) {
 __device__ __forceinline__ float kv8_scale_sum(float l, float half_factor) { return l * half_factor * half_factor; }
 
 // One tile of 16 keys at position pos0, rows at kr (and `tensor` bytes behind it the values), for NT groups of eight
-// heads.  meta: key scale times c1, value scale, its log2.  q: shared address of this lane's qhat operands, of each group's
-// head: 16-byte words at q ^ 64 i (kv8_q_place).
-// meta.y is the value scale times kWeightUp.
+// heads.  meta: key scale times c1, value scale times kWeightUp, log2 of the value scale.  q: shared address of this lane's qhat
+// operands, of each group's head: 16-byte words at q ^ 64 i (kv8_q_place).
 template <int D, int NT>
 __device__ __forceinline__ void kv8_tile(const uint8_t* kr, int tensor, int pos0, int lo, int n, const float4& meta,
                                          const uint32_t (&q)[NT], float (&o)[NT][D / 16][4], float (&m)[NT][2],
